@@ -73,7 +73,11 @@ typedef enum {
     MOE_CALL_COMBINE = 4,
     MOE_CALL_FORWARD = 5,
     MOE_CALL_ROUTER_STATS = 6,
-    MOE_CALL_FORWARD_FP8 = 7
+    MOE_CALL_FORWARD_FP8 = 7,
+    MOE_CALL_ADD_RMSNORM_BACKWARD = 8,
+    MOE_CALL_BALANCE_LOSS = 9, /* one sequence; see moe_balance_loss_workspace_size */
+    MOE_CALL_EXPERTS_W4 = 10,
+    MOE_CALL_FORWARD_W4 = 11
 } moe_call;
 
 typedef struct {
@@ -298,6 +302,175 @@ int32_t moe_forward_fp8(const moe_problem* problem, const void* x, const void* g
                         const uint8_t* shared_q, const float* shared_scale_gu,
                         const float* shared_scale_d, void* out, int32_t* topk_idx_out,
                         float* topk_w_out, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * moe_forward_fp8_encoded -- moe_forward_fp8 on token rows that are encoded
+ * already: x_q [T, H] E4M3 codes and x_scale [T] fp32 (device), as
+ * moe_add_rmsnorm writes them beside its bf16 rows.  The experts read the
+ * codes; the router reads x (bf16).  With the codes and scales that the
+ * encoding rule above gives for x the output equals moe_forward_fp8's bit for
+ * bit.  Everything else is as in moe_forward_fp8.
+ */
+int32_t moe_forward_fp8_encoded(const moe_problem* problem, const void* x, const uint8_t* x_q,
+                                const float* x_scale, const void* gate_w, const float* logit_bias,
+                                const uint8_t* expert_q, const float* expert_scale_gu,
+                                const float* expert_scale_d, const uint8_t* shared_q,
+                                const float* shared_scale_gu, const float* shared_scale_d,
+                                void* out, int32_t* topk_idx_out, float* topk_w_out,
+                                void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The layer's pre-norm.
+ *
+ * moe_add_rmsnorm -- residual addition and root-mean-square norm of T rows:
+ *   s[t]            = x[t] + residual[t]      (s = x without a residual)
+ *   residual_out[t] = s[t]                    in the problem dtype
+ *   y[t]            = s[t] * weight / sqrt(mean_h s[t]^2 + eps)
+ * computed in fp32 from the unrounded s and rounded once.  With y_q also the
+ * E4M3 codes of the rounded rows y with one power-of-two scale per row, by the
+ * rule moe_forward_fp8 encodes its rows with.
+ *   x, residual, residual_out, y [T, H] device (problem dtype); residual,
+ *            residual_out and y may be NULL (y only beside y_q)
+ *   weight   [H] device (problem dtype)
+ *   y_q      [T, H] uint8, y_scale [T] fp32 device: both or neither
+ * Each row is read before any of it is written, so residual_out and y may be
+ * x or residual themselves (in place), but not the same buffer.  Uses T, H and
+ * dtype of the problem; H <= 16384, eps >= 0.  No workspace.
+ */
+int32_t moe_add_rmsnorm(const moe_problem* problem, const void* x, const void* residual,
+                        const void* weight, float eps, void* residual_out, void* y, uint8_t* y_q,
+                        float* y_scale, void* stream);
+
+/*
+ * moe_add_rmsnorm_backward -- gradients of moe_add_rmsnorm, with
+ * h = residual_out as stored, r = (mean_h h^2 + eps)^-1/2 and g = dy * weight:
+ *   dx[t]   = r (g - h r mean_h(g h r)) + dresidual[t]    (the gradient of x
+ *             and of residual alike)
+ *   dweight = sum_t dy[t] h[t] r[t]
+ *   dy, dresidual, h, dx [T, H] device (problem dtype); dresidual (the gradient
+ *            of residual_out) may be NULL; dx may be dy or dresidual
+ *   dweight  [H] fp32 device, out, summed in a fixed order (reproducible); zero
+ *            for T = 0
+ * Workspace: MOE_CALL_ADD_RMSNORM_BACKWARD.  H <= 16384, eps >= 0.
+ */
+int32_t moe_add_rmsnorm_backward(const moe_problem* problem, const void* dy,
+                                 const void* dresidual, const void* h, const void* weight,
+                                 float eps, void* dx, float* dweight, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/*
+ * Balance loss with gradients, over packed sequences (the training form of the
+ * statistics of moe_router_stats; page "腾讯混元Hy3正式版深度解析",
+ * SparseMoERouter: the auxiliary load-balancing loss).
+ *
+ * Sequence s holds the tokens [seq_offsets[s], seq_offsets[s+1]) whose
+ * token_mask is nonzero, n_s of them; S sequences have n_s > 0.  With
+ * p_t = softmax(logits[t] + logit_bias):
+ *   mean_prob[s,e] = (1/n_s) sum_t p_t[e]                    (0 for n_s = 0)
+ *   counts[s,e]    = #{(t,j): topk_idx[t,j] == e}
+ *   loss           = (1/S) sum_s E sum_e mean_prob[s,e] counts[s,e]/(n_s top_k)
+ *                    (0 for S = 0)
+ *   tokens         = n_0 .. n_{n_seq-1}, then S
+ * For one sequence without a mask this is the aux_out of moe_router_stats.
+ *   logits      [T, E] fp32 device (moe_router_logits)
+ *   logit_bias  [E] fp32 device or NULL
+ *   topk_idx    [T, top_k] int32 device (moe_route)
+ *   token_mask  [T] uint8 device or NULL (every token counts)
+ *   seq_offsets [n_seq+1] int32 device, not decreasing, within [0, T]; NULL
+ *               with n_seq = 1: all T tokens.  Tokens outside every sequence
+ *               do not count.
+ *   loss [1] fp32, counts [n_seq, E] int32, tokens [n_seq+1] int32, mean_prob
+ *   [n_seq, E] fp32: device, out.
+ * Logits of tokens that do not count are not read.  Logits of -inf give
+ * probability 0; a token whose logits are all -inf has probability 0
+ * throughout.  Sums are taken in a fixed order (reproducible).  Offsets out of
+ * order and experts out of range set MOE_ERR_BAD_INDEX in the error word (such
+ * a sequence counts as empty, such a selection not at all).  1 <= n_seq <=
+ * 2^20.  Workspace: moe_balance_loss_workspace_size(problem, n_seq)
+ * (MOE_CALL_BALANCE_LOSS sizes it for n_seq = 1).
+ */
+size_t moe_balance_loss_workspace_size(const moe_problem* problem, int32_t n_seq);
+int32_t moe_balance_loss(const moe_problem* problem, const float* logits, const float* logit_bias,
+                         const int32_t* topk_idx, const uint8_t* token_mask,
+                         const int32_t* seq_offsets, int32_t n_seq, float* loss, int32_t* counts,
+                         int32_t* tokens, float* mean_prob, void* workspace, size_t ws_bytes,
+                         void* stream);
+
+/*
+ * moe_balance_loss_backward -- gradient of the balance loss with respect to
+ * the logits (the counts are piecewise constant and have none):
+ *   dlogits[t,e] = grad_loss[0] E/(S n_s) p_t[e] (f[e] - sum_j p_t[j] f[j]),
+ *   f[e] = counts[s,e] / (n_s top_k), s the token's sequence
+ * and 0 for tokens that do not count.  counts and tokens are those of
+ * moe_balance_loss on the same sequences and mask; grad_loss [1] fp32 device;
+ * dlogits [T, E] fp32 device, out.  No workspace.
+ */
+int32_t moe_balance_loss_backward(const moe_problem* problem, const float* logits,
+                                  const float* logit_bias, const uint8_t* token_mask,
+                                  const int32_t* seq_offsets, int32_t n_seq,
+                                  const int32_t* counts, const int32_t* tokens,
+                                  const float* grad_loss, float* dlogits, void* stream);
+
+/*
+ * 4-bit expert weights (page tqpw.cn/news/149001, section 6.1, names a
+ * checkpoint with 4-bit weights; the pages give no format).  A weight is
+ * (u - 8) * s: u its 4-bit code, s the bf16 scale of its group of group_size
+ * (32, 64 or 128) consecutive weights along the contraction (H for gate and
+ * up, I for down).  Activations stay bf16, sums fp32.  H and I must be
+ * multiples of 128.
+ *
+ * Packed layout, per expert: 3*I*H/2 bytes of codes and 3*I*H/group_size
+ * scales, the gate/up part (I*H bytes, 2*I*H/group_size scales) before the
+ * down part.  A part is cut into pair tiles of 32 rows (gate/up tile j: gate
+ * rows 16j..16j+15, then up rows 16j..16j+15; down tile j: outputs 32j..32j+31)
+ * and blocks of 128 along the contraction:
+ *   codes  [tile][block][half 2][lane 32][byte 32]
+ *          byte b of lane 4r+c: row r of the half in its low nibble, row r+8
+ *          in its high one, at k = 32 (b/8) + 8 c + 4 (b/4 % 2) +
+ *          {0, 2, 1, 3}[b % 4] of the block
+ *   scales [tile][block][r 8][128/group_size][half 2][r, r+8]
+ *
+ * moe_quantize_weights_w4 -- encode [n_experts, 3, I, H] weights (problem
+ * dtype, device; layout as in moe_grouped_swiglu_ffn) into q and scales
+ * (device).  s = max|w| / 7 of the group, rounded to fp32 and then to bf16 (1
+ * where that is 0; NaN where the group holds a value that is not finite),
+ * u - 8 = w/s rounded to nearest, ties to even, held to [-7, 7].
+ */
+int32_t moe_quantize_weights_w4(const moe_problem* problem, int32_t group_size,
+                                int32_t n_experts, const void* w, uint8_t* q, void* scales,
+                                void* stream);
+
+/*
+ * moe_experts_w4 -- the layer behind its router, with 4-bit expert weights:
+ *   out[t] = sum_j topk_w[t,j] * FFN_{topk_idx[t,j]}(x[t])  (+ shared FFN(x[t]))
+ * dispatch, gate/up + clamp + SwiGLU, down, and the fixed-order combine in
+ * fp32 (reproducible).  For decoding: the products are bound by reading the
+ * weights of the touched experts up to about 8 rows per expert.
+ *   x, out [T, H] bf16; topk_idx [T, top_k] int32 (a token's experts distinct);
+ *   topk_w [T, top_k] fp32; expert_q, expert_scale: E experts;
+ *   shared_q, shared_scale: 1 expert, or NULL when num_shared == 0.
+ *   expert_q and shared_q are 32-byte aligned.
+ * An expert out of range sets MOE_ERR_BAD_INDEX in the error word and adds
+ * nothing; so does (setting it) an expert that a token lists twice, and that
+ * token's row is then not defined.  dtype MOE_BF16.  Workspace:
+ * MOE_CALL_EXPERTS_W4.
+ */
+int32_t moe_experts_w4(const moe_problem* problem, int32_t group_size, const void* x,
+                       const int32_t* topk_idx, const float* topk_w, const uint8_t* expert_q,
+                       const void* expert_scale, const uint8_t* shared_q,
+                       const void* shared_scale, void* out, void* workspace, size_t ws_bytes,
+                       void* stream);
+
+/*
+ * moe_forward_w4 -- moe_route and moe_experts_w4 in one call; arguments as in
+ * moe_forward with the weights of moe_quantize_weights_w4.  Workspace:
+ * MOE_CALL_FORWARD_W4.
+ */
+int32_t moe_forward_w4(const moe_problem* problem, int32_t group_size, const void* x,
+                       const void* gate_w, const float* logit_bias, const uint8_t* expert_q,
+                       const void* expert_scale, const uint8_t* shared_q,
+                       const void* shared_scale, void* out, int32_t* topk_idx_out,
+                       float* topk_w_out, void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * moe_check_wait_timeout -- self-check of the bounded waits every kernel uses

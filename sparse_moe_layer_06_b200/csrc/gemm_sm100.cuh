@@ -46,48 +46,13 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "device_common.cuh"
 #include "ptx.cuh"
 #include "route_topk.cuh"
 
 namespace moe {
 
 enum EpiKind : int { EPI_LOGITS = 0, EPI_SWIGLU = 1, EPI_DOWN_ATOMIC = 2, EPI_DOWN_STORE = 3 };
-
-enum DeviceError : int { DEV_OK = 0, DEV_ERR_TIMEOUT = 5, DEV_ERR_BAD_INDEX = 6 };
-
-__device__ __forceinline__ void set_device_error(int32_t* status, int code) {
-    if (status) atomicCAS(status, 0, code);
-}
-
-// Device-built tile schedule for nseg segments (a segment = the rows that
-// share one weight matrix).  int32 array of 5*(nseg+1) entries:
-//   prefix[nseg+1]  exclusive prefix sum of per-segment chunk counts
-//   b_row0[nseg]    first row of the segment in its B tensor map
-//   out_row0[nseg]  first row of the segment in the output row space
-//   rows[nseg]      rows in the segment
-//   chunk_len[nseg] rows per chunk (multiple of 16, <= NMAX)
-// Tiles are ordered (segment, chunk, weight block) with the weight block
-// fastest, so the CTAs working at the same time share one chunk of token rows
-// and, across neighbouring chunks, the same weight blocks through L2.
-struct SchedPtrs {
-    const int32_t* prefix;
-    const int32_t* b_row0;
-    const int32_t* out_row0;
-    const int32_t* rows;
-    const int32_t* chunk_len;
-};
-
-__host__ __device__ inline SchedPtrs sched_ptrs(const int32_t* base, int nseg) {
-    SchedPtrs p;
-    p.prefix = base;
-    p.b_row0 = base + (nseg + 1);
-    p.out_row0 = base + 2 * (nseg + 1);
-    p.rows = base + 3 * (nseg + 1);
-    p.chunk_len = base + 4 * (nseg + 1);
-    return p;
-}
-
-constexpr int kMaxSegments = 257;  // 256 routed experts + 1 shared expert
 
 // Token rows are fetched with TMA boxes of 16 << j rows (j = 0..4): a tile of
 // n rows (a multiple of 16) takes one box per set bit of n/16, so a typical

@@ -1,84 +1,19 @@
 // moe_api.cu -- host side of the C ABI declared in include/moe.h:
-// argument validation, workspace carving, TMA tensor-map encoding, kernel
-// launch sequencing, the launch counter and the per-kernel event profiler.
+// argument validation, workspace layouts, TMA tensor-map encoding and kernel
+// launch sequencing.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
-#include <cmath>
-#include <cstdint>
-#include <cstdlib>
 #include <cstring>
-#include <mutex>
-#include <utility>
-#include <vector>
 
-#include "../../include/moe.h"
+#include "host_common.cuh"
+#include "internal.hpp"
 #include "gemm_sm100.cuh"
 #include "small_kernels.cuh"
 
 namespace moe {
 namespace {
-
-// ------------------------------------------------------------------ launch bookkeeping
-
-std::atomic<int64_t> g_launches{0};
-
-struct ProfRecord {
-    const char* name;
-    cudaEvent_t start, stop;
-};
-
-struct Profiler {
-    std::mutex mu;
-    bool on = false;
-    std::vector<cudaEvent_t> pool;  // 2 per record
-    std::vector<ProfRecord> recs;
-    size_t cap = 0;
-};
-Profiler g_prof;
-
-struct LaunchScope {
-    cudaEvent_t stop = nullptr;
-    cudaStream_t stream;
-    LaunchScope(const char* name, cudaStream_t s) : stream(s) {
-        if (!g_prof.on) return;
-        std::lock_guard<std::mutex> lk(g_prof.mu);
-        if (!g_prof.on || g_prof.recs.size() >= g_prof.cap) return;
-        ProfRecord r{name, g_prof.pool[2 * g_prof.recs.size()],
-                     g_prof.pool[2 * g_prof.recs.size() + 1]};
-        cudaEventRecord(r.start, s);
-        stop = r.stop;
-        g_prof.recs.push_back(r);
-    }
-    ~LaunchScope() {
-        g_launches.fetch_add(1, std::memory_order_relaxed);
-        if (stop) cudaEventRecord(stop, stream);
-    }
-};
-
-#define MOE_LAUNCH(name, stream, ...)              \
-    do {                                           \
-        LaunchScope scope_(name, stream);          \
-        __VA_ARGS__;                               \
-        cudaError_t e_ = cudaGetLastError();       \
-        if (e_ != cudaSuccess) return MOE_ERR_CUDA; \
-    } while (0)
-
-// ------------------------------------------------------------------ device info
-
-int sm_count() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-    static int cache[64] = {0};
-    if (dev < 64 && cache[dev]) return cache[dev];
-    int n = 0;
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (n <= 0) n = 148;
-    if (dev < 64) cache[dev] = n;
-    return n;
-}
 
 // ------------------------------------------------------------------ tensor maps
 
@@ -111,8 +46,6 @@ struct ElemType {
 constexpr ElemType kBF16{CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2};
 constexpr ElemType kU8{CU_TENSOR_MAP_DATA_TYPE_UINT8, 1};
 constexpr ElemType kF32{CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4};
-
-int env_int(const char* name, int dflt);
 
 // L2 sector promotion of the expert-weight tensor maps (MOE_L2_PROMO: 0 none,
 // 1 64 B, 2 128 B, 3 256 B; default 256 B).  A weight tile row is 128 bytes
@@ -200,34 +133,10 @@ bool make_tmap_rows(CUtensorMap* maps, const void* ptr, int64_t rows, int64_t co
 
 // ------------------------------------------------------------------ problem checks
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int32_t check_problem(const moe_problem* p) {
-    if (!p) return MOE_ERR_INVALID_ARG;
-    if (p->T < 0) return MOE_ERR_INVALID_ARG;
-    if (p->dtype != MOE_F32 && p->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
-    if (p->H < 64 || p->H % 64 != 0 || p->I < 64 || p->I % 64 != 0) return MOE_ERR_UNSUPPORTED;
-    // top_k <= 32: the router and the row gather keep one selection per lane
-    if (p->E < 1 || p->E > kMaxExperts || p->top_k < 1 || p->top_k > p->E || p->top_k > 32)
-        return MOE_ERR_UNSUPPORTED;
-    if (p->num_shared != 0 && p->num_shared != 1) return MOE_ERR_UNSUPPORTED;
-    if (p->T * static_cast<int64_t>(p->top_k + p->num_shared) >= (int64_t(1) << 31))
-        return MOE_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(p->E) * 3 * p->I >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
-    if (!std::isfinite(p->routed_scale)) return MOE_ERR_INVALID_ARG;
-    if (std::isnan(p->clip_limit)) return MOE_ERR_INVALID_ARG;
-    return MOE_OK;
-}
-
 float effective_clip(const moe_problem* p) {
     return (p->clip_limit > 0.0f && std::isfinite(p->clip_limit)) ? p->clip_limit : INFINITY;
 }
 
-
-int env_int(const char* name, int dflt) {
-    const char* e = std::getenv(name);
-    return e ? std::atoi(e) : dflt;
-}
 
 bool nmax_supported(int n) {
     return n == 16 || n == 32 || n == 64 || n == 128 || n == 160 || n == 256;
@@ -312,15 +221,6 @@ int64_t logits_chunks(const moe_problem* p) {
 }
 
 // ------------------------------------------------------------------ workspace layout
-
-struct Carve {
-    size_t off = 0;
-    size_t take(size_t bytes) {
-        size_t o = off;
-        off += (bytes + 255) & ~size_t(255);
-        return o;
-    }
-};
 
 struct Layout {
     size_t status, logits, rcount, idx, w, hist, base, counts, offsets, partial, sched_gu, sched_dn,
@@ -414,32 +314,7 @@ Layout layout_for(const moe_problem* p, int call, int64_t ffn_rows = 0, int ffn_
     return L;
 }
 
-template <typename T>
-T* at(void* ws, size_t off) {
-    return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
-}
-
 // ------------------------------------------------------------------ GEMM launch
-
-// Kernel launch on stream s; with pdl the launch may begin before the
-// previous launch on the stream has finished (programmatic stream
-// serialization): the kernel must then wait (griddepcontrol.wait) before it
-// reads anything the previous launch writes.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_ex(void (*kern)(KArgs...), int grid, int threads, int smem, cudaStream_t s,
-                      bool pdl, Args&&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
-}
 
 // Clusters of two CTAs (one per SM) of `kern` that can be resident at once.
 template <typename K>
@@ -695,15 +570,6 @@ int l2_hints() {
 // were already evenly loaded), so the plain order is the default.
 int k_rotate() {
     const int v = env_int("MOE_KROT", 0) ? 1 : 0;
-    return v;
-}
-
-// Programmatic dependent launch along the forward's kernel chain (MOE_PDL=0
-// turns it off): each kernel may start while its predecessor finishes, does
-// its independent set-up (in the expert GEMMs: streams its first weight
-// tiles), then waits for the predecessor before reading its outputs.
-bool pdl_enabled() {
-    const bool v = env_int("MOE_PDL", 1) != 0;
     return v;
 }
 
@@ -1006,13 +872,26 @@ int32_t run_finalize(const float* acc, TOut* out, int64_t n, cudaStream_t s, boo
     return MOE_OK;
 }
 
-#define MOE_TRY(expr)                      \
-    do {                                   \
-        int32_t r_ = (expr);               \
-        if (r_ != MOE_OK) return r_;       \
-    } while (0)
-
 }  // namespace
+
+int32_t dispatch_rows(const moe_problem* p, const int32_t* idx, const float* topk_w,
+                      int32_t* hist, int32_t* base, int32_t* counts, int32_t* offsets,
+                      int32_t* sched_gu, int nmax_gu, int32_t* sched_dn, int nmax_dn,
+                      int32_t* pos, int32_t* src, float* row_w, int32_t* status, cudaStream_t s) {
+    return run_dispatch(p, idx, topk_w, hist, base, counts, offsets, sched_gu, nmax_gu, sched_dn,
+                        nmax_dn, pos, src, row_w, status, s);
+}
+
+int64_t dispatch_chunks(int64_t T) { return perm_chunks(T); }
+size_t schedule_bytes() { return sched_bytes(); }
+
+int32_t combine_rows_f32(const moe_problem* p, const float* y, const int32_t* pos,
+                         __nv_bfloat16* out, int32_t* status, cudaStream_t s) {
+    const int64_t n_rows = p->T * p->top_k;
+    return run_gather_sum(y, pos, p->T, p->H, p->top_k, n_rows, p->num_shared ? n_rows : -1, out,
+                          status, s, pdl_enabled());
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -1034,7 +913,8 @@ const char* moe_status_string(int32_t status) {
 
 size_t moe_workspace_size(const moe_problem* p, int32_t call) {
     if (check_problem(p) != MOE_OK) return 0;
-    if (call < MOE_CALL_ROUTE || call > MOE_CALL_FORWARD_FP8) return 0;
+    if (call < MOE_CALL_ROUTE || call > MOE_CALL_FORWARD_W4) return 0;
+    if (call > MOE_CALL_FORWARD_FP8) return operator_workspace(p, call);
     if (call == MOE_CALL_FFN) {
         // the FFN workspace depends on rows/groups; size it for the routed
         // rows of this problem (T*top_k) and E groups, the larger of the two
@@ -1519,8 +1399,9 @@ int32_t moe_quantize_weights_fp8(const moe_problem* p, int32_t n_experts, const 
     return MOE_OK;
 }
 
-int32_t moe_forward_fp8(const moe_problem* p, const void* x, const void* gate_w,
-                        const float* bias, const uint8_t* expert_q, const float* expert_s_gu,
+// x_q and x_s: the token rows' codes and scales, or null to encode x here.
+static int32_t forward_fp8(const moe_problem* p, const void* x, const uint8_t* x_q_in,
+                           const float* x_s_in, const void* gate_w, const float* bias, const uint8_t* expert_q, const float* expert_s_gu,
                         const float* expert_s_d, const uint8_t* shared_q,
                         const float* shared_s_gu, const float* shared_s_d, void* out,
                         int32_t* idx_out, float* w_out, void* ws, size_t ws_bytes,
@@ -1559,12 +1440,18 @@ int32_t moe_forward_fp8(const moe_problem* p, const void* x, const void* gate_w,
                          at<int32_t>(ws, L.counts), at<int32_t>(ws, L.offsets), sg, nmax, sd,
                          nmax_dn, pos, src, row_w, status, s));
     // 3. token rows to E4M3 with a power-of-two scale per token, then permuted
-    uint8_t* x_q = at<uint8_t>(ws, L.x_q);
-    float* s_x = at<float>(ws, L.s_x);
-    MOE_LAUNCH("quantize_tokens", s,
-               quantize_rows_e4m3_kernel<__nv_bfloat16><<<static_cast<unsigned>((T + 7) / 8), 256,
-                                                          0, s>>>(
-                   static_cast<const __nv_bfloat16*>(x), T, static_cast<int>(H), T, T, x_q, s_x));
+    const uint8_t* x_q = x_q_in;
+    const float* s_x = x_s_in;
+    if (!x_q) {
+        uint8_t* q = at<uint8_t>(ws, L.x_q);
+        float* sc = at<float>(ws, L.s_x);
+        MOE_LAUNCH("quantize_tokens", s,
+                   quantize_rows_e4m3_kernel<__nv_bfloat16><<<static_cast<unsigned>((T + 7) / 8),
+                                                              256, 0, s>>>(
+                       static_cast<const __nv_bfloat16*>(x), T, static_cast<int>(H), T, T, q, sc));
+        x_q = q;
+        s_x = sc;
+    }
     uint8_t* x_perm = at<uint8_t>(ws, L.x_perm);
     const bool pdl = pdl_enabled();
     // the gate/up GEMM's gather warps fetch the code rows straight from x_q
@@ -1658,6 +1545,30 @@ int32_t moe_forward_fp8(const moe_problem* p, const void* x, const void* gate_w,
     return run_gather_sum(static_cast<const __nv_bfloat16*>(y_perm), pos, T, p->H, p->top_k,
                           T * k, S ? T * k : -1, static_cast<__nv_bfloat16*>(out), status, s,
                           pdl);
+}
+
+int32_t moe_forward_fp8(const moe_problem* p, const void* x, const void* gate_w,
+                        const float* bias, const uint8_t* expert_q, const float* expert_s_gu,
+                        const float* expert_s_d, const uint8_t* shared_q,
+                        const float* shared_s_gu, const float* shared_s_d, void* out,
+                        int32_t* idx_out, float* w_out, void* ws, size_t ws_bytes,
+                        void* stream) {
+    return forward_fp8(p, x, nullptr, nullptr, gate_w, bias, expert_q, expert_s_gu, expert_s_d,
+                       shared_q, shared_s_gu, shared_s_d, out, idx_out, w_out, ws, ws_bytes,
+                       stream);
+}
+
+int32_t moe_forward_fp8_encoded(const moe_problem* p, const void* x, const uint8_t* x_q,
+                                const float* x_scale, const void* gate_w, const float* bias,
+                                const uint8_t* expert_q, const float* expert_s_gu,
+                                const float* expert_s_d, const uint8_t* shared_q,
+                                const float* shared_s_gu, const float* shared_s_d, void* out,
+                                int32_t* idx_out, float* w_out, void* ws, size_t ws_bytes,
+                                void* stream) {
+    if (!x_q || !x_scale || !aligned16(x_q)) return MOE_ERR_INVALID_ARG;
+    return forward_fp8(p, x, x_q, x_scale, gate_w, bias, expert_q, expert_s_gu, expert_s_d,
+                       shared_q, shared_s_gu, shared_s_d, out, idx_out, w_out, ws, ws_bytes,
+                       stream);
 }
 
 int32_t moe_read_device_status(const void* ws, int32_t* status_out, void* stream) {

@@ -1,0 +1,460 @@
+// ops_api.cu -- host side of the operators around the layer: the pre-norm and
+// its backward pass, the balance loss and its gradient, and the experts'
+// products with 4-bit weights.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "host_common.cuh"
+#include "internal.hpp"
+#include "balance_kernels.cuh"
+#include "norm_kernels.cuh"
+#include "w4_kernels.cuh"
+
+namespace moe {
+namespace {
+
+// ------------------------------------------------------------------ norm
+
+int32_t check_norm(const moe_problem* p, float eps) {
+    MOE_TRY(check_problem(p));
+    if (p->H > kNormMaxH) return MOE_ERR_UNSUPPORTED;
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+// Threads of one row: kNormVec vectors each, whole warps.
+int norm_threads(const moe_problem* p) {
+    const int nv = p->H * (p->dtype == MOE_BF16 ? 2 : 4) / 16;
+    return std::max(32, ((nv + kNormVec - 1) / kNormVec + 31) / 32 * 32);
+}
+
+template <typename T>
+int32_t run_norm(const moe_problem* p, const void* x, const void* res, const void* weight,
+                 float eps, void* res_out, void* y, uint8_t* y_q, float* y_scale,
+                 cudaStream_t s) {
+    const int nt = norm_threads(p);
+    const bool warp = nt == 32;
+    const int threads = warp ? 128 : nt;
+    const int64_t rows = warp ? (p->T + 3) / 4 : p->T;
+    auto kern = warp ? add_rmsnorm_kernel<T, true> : add_rmsnorm_kernel<T, false>;
+    MOE_LAUNCH("add_rmsnorm", s,
+               if (launch_ex(kern, static_cast<int>(rows), threads, 0, s, pdl_enabled(),
+                             static_cast<const T*>(x), static_cast<const T*>(res),
+                             static_cast<const T*>(weight), eps, p->T, p->H,
+                             static_cast<T*>(res_out), static_cast<T*>(y), y_q, y_scale) !=
+                   cudaSuccess) return MOE_ERR_CUDA);
+    return MOE_OK;
+}
+
+// CTAs of the backward pass: as many rows for each, and about kNormBackCtas
+// CTAs (the workspace holds a partial dw of each).
+constexpr int64_t kNormBackCtas = 148 * 3;
+int64_t norm_backward_ctas(int64_t T) {
+    if (T <= 0) return 1;
+    const int64_t per = (T + kNormBackCtas - 1) / kNormBackCtas;
+    return (T + per - 1) / per;
+}
+
+template <typename T>
+int32_t run_norm_backward(const moe_problem* p, const void* dy, const void* dres, const void* h,
+                          const void* weight, float eps, void* dx, float* dweight,
+                          float* partial, cudaStream_t s) {
+    const int ctas = static_cast<int>(norm_backward_ctas(p->T));
+    MOE_LAUNCH("add_rmsnorm_backward", s,
+               if (launch_ex(add_rmsnorm_backward_kernel<T>, ctas, norm_threads(p), 0, s,
+                             pdl_enabled(), static_cast<const T*>(dy),
+                             static_cast<const T*>(dres), static_cast<const T*>(h),
+                             static_cast<const T*>(weight), eps, p->T, p->H,
+                             static_cast<T*>(dx), partial) != cudaSuccess) return MOE_ERR_CUDA);
+    MOE_LAUNCH("add_rmsnorm_dweight", s,
+               if (launch_ex(reduce_columns_kernel, p->H / 32, 256, 0, s, pdl_enabled(),
+                             static_cast<const float*>(partial), ctas, p->H, dweight) !=
+                   cudaSuccess) return MOE_ERR_CUDA);
+    return MOE_OK;
+}
+
+// ------------------------------------------------------------------ balance loss
+
+constexpr int32_t kMaxSequences = 1 << 20;
+
+// Tokens per window: whole rounds of the CTA's 8 warps, about 4 windows per SM.
+int balance_window(int64_t T) {
+    return static_cast<int>(8 * std::max<int64_t>(1, (T + 8 * 592 - 1) / (8 * 592)));
+}
+
+struct BalanceLayout {
+    size_t status, ticket, part_p, part_c, part_n, seq_loss, total;
+};
+
+BalanceLayout balance_layout(const moe_problem* p, int64_t n_seq) {
+    BalanceLayout L{};
+    Carve c;
+    const int64_t win = balance_window(p->T);
+    const int64_t slots = std::max<int64_t>(1, (p->T + win - 1) / win) + n_seq;
+    L.status = c.take(256);
+    L.ticket = c.take(4);
+    L.part_p = c.take(slots * p->E * 4);
+    L.part_c = c.take(slots * p->E * 4);
+    L.part_n = c.take(slots * 4);
+    L.seq_loss = c.take(n_seq * 8);
+    L.total = c.off;
+    return L;
+}
+
+int32_t check_sequences(const int32_t* offsets, int32_t n_seq) {
+    if (n_seq < 1 || (!offsets && n_seq != 1)) return MOE_ERR_INVALID_ARG;
+    if (n_seq > kMaxSequences) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// ------------------------------------------------------------------ 4-bit experts
+
+int32_t check_w4(const moe_problem* p, int32_t group) {
+    MOE_TRY(check_problem(p));
+    if (p->H % kW4Block != 0 || p->I % kW4Block != 0) return MOE_ERR_UNSUPPORTED;
+    if (group != 32 && group != 64 && group != 128) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+struct W4Layout {
+    size_t status, route, idx, w, hist, base, counts, offsets, sched_gu, sched_dn, pos, src,
+        row_w, h, y, total;
+};
+
+W4Layout w4_layout(const moe_problem* p, bool with_route) {
+    W4Layout L{};
+    Carve c;
+    const int64_t T = p->T, H = p->H, E = p->E, I = p->I, k = p->top_k, S = p->num_shared;
+    // the router's workspace (error word first), or the error word alone
+    L.status = c.take(with_route ? moe_workspace_size(p, MOE_CALL_ROUTE) : 256);
+    if (with_route) {
+        L.idx = c.take(T * k * 4);
+        L.w = c.take(T * k * 4);
+    }
+    L.hist = c.take(dispatch_chunks(T) * E * 4);
+    L.base = c.take(dispatch_chunks(T) * E * 4);
+    L.counts = c.take(E * 4);
+    L.offsets = c.take((E + 1) * 4);
+    L.sched_gu = c.take(schedule_bytes());
+    L.sched_dn = c.take(schedule_bytes());
+    L.pos = c.take(T * k * 4);
+    L.src = c.take(T * k * 4);
+    L.row_w = c.take(T * k * 4);
+    L.h = c.take(T * (k + S) * I * 4);  // bf16 high and low parts
+    L.y = c.take(T * (k + S) * H * 4);
+    L.total = c.off;
+    return L;
+}
+
+// 8-row column tiles per task, from the mean rows per expert.
+int w4_column_tiles(double mean_rows) {
+    if (mean_rows <= 3.0) return 1;
+    if (mean_rows <= 10.0) return 2;
+    return 4;
+}
+
+template <int NT, bool DOWN, int SUB>
+int32_t launch_w4_n(const W4Args& a, int64_t max_tasks, cudaStream_t s) {
+    auto kern = w4_product_kernel<NT, DOWN, SUB>;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    static std::atomic<int> per_sm[64];
+    int n = dev < 64 ? per_sm[dev].load() : 0;
+    if (n == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kW4Threads, 0) !=
+                cudaSuccess ||
+            n < 1)
+            return MOE_ERR_CUDA;
+        if (dev < 64) per_sm[dev].store(n);
+    }
+    const int64_t warps = kW4Threads / 32;
+    const int grid = static_cast<int>(
+        std::max<int64_t>(1, std::min<int64_t>(static_cast<int64_t>(sm_count()) * n,
+                                               (max_tasks + warps - 1) / warps)));
+    MOE_LAUNCH(DOWN ? "expert_down_w4" : "expert_gate_up_w4", s,
+               if (launch_ex(kern, grid, kW4Threads, 0, s, pdl_enabled(), a) != cudaSuccess)
+                   return MOE_ERR_CUDA);
+    return MOE_OK;
+}
+
+template <bool DOWN>
+int32_t launch_w4(int nt, int group, const W4Args& a, int64_t max_tasks, cudaStream_t s) {
+    const int key = nt * 1000 + group;
+    switch (key) {
+        case 1032: return launch_w4_n<1, DOWN, 4>(a, max_tasks, s);
+        case 1064: return launch_w4_n<1, DOWN, 2>(a, max_tasks, s);
+        case 1128: return launch_w4_n<1, DOWN, 1>(a, max_tasks, s);
+        case 2032: return launch_w4_n<2, DOWN, 4>(a, max_tasks, s);
+        case 2064: return launch_w4_n<2, DOWN, 2>(a, max_tasks, s);
+        case 2128: return launch_w4_n<2, DOWN, 1>(a, max_tasks, s);
+        case 4032: return launch_w4_n<4, DOWN, 4>(a, max_tasks, s);
+        case 4064: return launch_w4_n<4, DOWN, 2>(a, max_tasks, s);
+        case 4128: return launch_w4_n<4, DOWN, 1>(a, max_tasks, s);
+        default: return MOE_ERR_UNSUPPORTED;
+    }
+}
+
+int32_t run_experts_w4(const moe_problem* p, int32_t group, const void* x, const int32_t* idx,
+                       const float* w, const uint8_t* eq, const void* es, const uint8_t* sq,
+                       const void* ss, void* out, void* ws, const W4Layout& L, cudaStream_t s) {
+    const int64_t T = p->T, H = p->H, E = p->E, I = p->I, k = p->top_k, S = p->num_shared;
+    int32_t* status = at<int32_t>(ws, L.status);
+    int32_t* sg = at<int32_t>(ws, L.sched_gu);
+    int32_t* sd = at<int32_t>(ws, L.sched_dn);
+    int32_t* pos = at<int32_t>(ws, L.pos);
+    int32_t* src = at<int32_t>(ws, L.src);
+    float* row_w = at<float>(ws, L.row_w);
+    const int nt = w4_column_tiles(static_cast<double>(T * k) / E);
+    const bool pdl = pdl_enabled();
+    if (T <= kPermTokens) {
+        MOE_LAUNCH("dispatch_w4", s,
+                   if (launch_ex(w4_dispatch_kernel, 1, 512, 0, s, pdl, idx, w,
+                                 static_cast<int>(T), p->E, p->top_k, p->num_shared, 8 * nt, sg,
+                                 sd, pos, src, row_w, status) != cudaSuccess)
+                       return MOE_ERR_CUDA);
+    } else {
+        // (an assignment with an expert out of range keeps position -1)
+        if (cudaMemsetAsync(pos, 0xff, static_cast<size_t>(T * k) * 4, s) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        MOE_TRY(dispatch_rows(p, idx, w, at<int32_t>(ws, L.hist), at<int32_t>(ws, L.base),
+                              at<int32_t>(ws, L.counts), at<int32_t>(ws, L.offsets), sg, 8 * nt,
+                              sd, 8 * nt, pos, src, row_w, status, s));
+    }
+    const int nseg = static_cast<int>(E + S);
+    // at most this many chunks of 8 nt rows over all segments
+    const int64_t chunks = std::min<int64_t>(T * k, T * k / (8 * nt) + E) +
+                           (S ? (T + 8 * nt - 1) / (8 * nt) : 0);
+    W4Args a{};
+    a.nseg = nseg;
+    a.special = S ? static_cast<int32_t>(E) : -1;
+    a.q_stride = 3 * I * H / 2;
+    a.sc_stride = 3 * I * H / group;
+    a.routed_rows = static_cast<int32_t>(T * k);
+    a.row_w = row_w;
+    a.row_src = src;
+    a.clip = (p->clip_limit > 0.0f && std::isfinite(p->clip_limit)) ? p->clip_limit : INFINITY;
+    a.q = eq;
+    a.sc = static_cast<const __nv_bfloat16*>(es);
+    a.q_shared = sq;
+    a.sc_shared = static_cast<const __nv_bfloat16*>(ss);
+    a.sched = sg;
+    a.rows = static_cast<const __nv_bfloat16*>(x);
+    a.K = static_cast<int32_t>(H);
+    a.tiles = static_cast<int32_t>(I / 16);
+    a.out = at<void>(ws, L.h);
+    a.ld = static_cast<int32_t>(I);
+    MOE_TRY(launch_w4<false>(nt, group, a, chunks * a.tiles, s));
+    a.q = eq + I * H;
+    a.sc = static_cast<const __nv_bfloat16*>(es) + 2 * I * H / group;
+    a.q_shared = sq ? sq + I * H : nullptr;
+    a.sc_shared = ss ? static_cast<const __nv_bfloat16*>(ss) + 2 * I * H / group : nullptr;
+    a.sched = sd;
+    a.rows = at<__nv_bfloat16>(ws, L.h);
+    a.K = static_cast<int32_t>(I);
+    a.tiles = static_cast<int32_t>(H / 32);
+    a.out = at<void>(ws, L.y);
+    a.ld = static_cast<int32_t>(H);
+    MOE_TRY(launch_w4<true>(nt, group, a, chunks * a.tiles, s));
+    return combine_rows_f32(p, at<float>(ws, L.y), pos, static_cast<__nv_bfloat16*>(out), status,
+                            s);
+}
+
+bool aligned32(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 31u) == 0; }
+
+// Checks of the two 4-bit entry points.
+int32_t check_w4_call(const moe_problem* p, int32_t group, const void* x, const uint8_t* eq,
+                      const void* es, const uint8_t* sq, const void* ss, const void* out,
+                      const void* ws) {
+    MOE_TRY(check_w4(p, group));
+    if (p->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+    if (!x || !eq || !es || !out || !ws) return MOE_ERR_INVALID_ARG;
+    if (p->num_shared && (!sq || !ss)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(eq) || !aligned16(es) || !aligned16(out) || !aligned16(ws) ||
+        (sq && !aligned16(sq)) || (ss && !aligned16(ss)))
+        return MOE_ERR_INVALID_ARG;
+    // the codes are read in 32-byte vectors
+    if (!aligned32(eq) || (sq && !aligned32(sq))) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+}  // namespace
+
+size_t operator_workspace(const moe_problem* p, int32_t call) {
+    switch (call) {
+        case MOE_CALL_ADD_RMSNORM_BACKWARD:
+            if (p->H > kNormMaxH) return 0;
+            return 256 + static_cast<size_t>(norm_backward_ctas(p->T)) * p->H * 4;
+        case MOE_CALL_BALANCE_LOSS: return balance_layout(p, 1).total;
+        case MOE_CALL_EXPERTS_W4:
+        case MOE_CALL_FORWARD_W4:
+            if (check_w4(p, kW4Block) != MOE_OK || p->dtype != MOE_BF16) return 0;
+            return w4_layout(p, call == MOE_CALL_FORWARD_W4).total;
+        default: return 0;
+    }
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int32_t moe_add_rmsnorm(const moe_problem* p, const void* x, const void* residual,
+                        const void* weight, float eps, void* residual_out, void* y, uint8_t* y_q,
+                        float* y_scale, void* stream) {
+    MOE_TRY(check_norm(p, eps));
+    if (!x || !weight || (!y && !y_q) || (!y_q) != (!y_scale)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) ||
+        !aligned16(y) || !aligned16(y_q))
+        return MOE_ERR_INVALID_ARG;
+    if (p->T == 0) return MOE_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p->dtype == MOE_BF16)
+        return run_norm<__nv_bfloat16>(p, x, residual, weight, eps, residual_out, y, y_q, y_scale,
+                                       s);
+    return run_norm<float>(p, x, residual, weight, eps, residual_out, y, y_q, y_scale, s);
+}
+
+int32_t moe_add_rmsnorm_backward(const moe_problem* p, const void* dy, const void* dresidual,
+                                 const void* h, const void* weight, float eps, void* dx,
+                                 float* dweight, void* ws, size_t ws_bytes, void* stream) {
+    MOE_TRY(check_norm(p, eps));
+    if (!dy || !h || !weight || !dx || !dweight || !ws) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(dresidual) || !aligned16(h) || !aligned16(weight) ||
+        !aligned16(dx) || !aligned16(ws))
+        return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < operator_workspace(p, MOE_CALL_ADD_RMSNORM_BACKWARD)) return MOE_ERR_WORKSPACE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p->T == 0) {
+        // the sum over no rows
+        if (cudaMemsetAsync(dweight, 0, static_cast<size_t>(p->H) * 4, s) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    float* partial = at<float>(ws, 256);
+    if (p->dtype == MOE_BF16)
+        return run_norm_backward<__nv_bfloat16>(p, dy, dresidual, h, weight, eps, dx, dweight,
+                                                partial, s);
+    return run_norm_backward<float>(p, dy, dresidual, h, weight, eps, dx, dweight, partial, s);
+}
+
+size_t moe_balance_loss_workspace_size(const moe_problem* p, int32_t n_seq) {
+    if (check_problem(p) != MOE_OK || n_seq < 1 || n_seq > kMaxSequences) return 0;
+    return balance_layout(p, n_seq).total;
+}
+
+int32_t moe_balance_loss(const moe_problem* p, const float* logits, const float* bias,
+                         const int32_t* topk_idx, const uint8_t* token_mask,
+                         const int32_t* seq_offsets, int32_t n_seq, float* loss, int32_t* counts,
+                         int32_t* tokens, float* mean_prob, void* ws, size_t ws_bytes,
+                         void* stream) {
+    MOE_TRY(check_problem(p));
+    MOE_TRY(check_sequences(seq_offsets, n_seq));
+    if (!logits || !topk_idx || !loss || !counts || !tokens || !mean_prob || !ws)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
+    const BalanceLayout L = balance_layout(p, n_seq);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int win = balance_window(p->T);
+    const int nwin = static_cast<int>(std::max<int64_t>(1, (p->T + win - 1) / win));
+    int32_t* status = at<int32_t>(ws, L.status);
+    float* part_p = at<float>(ws, L.part_p);
+    int32_t* part_c = at<int32_t>(ws, L.part_c);
+    int32_t* part_n = at<int32_t>(ws, L.part_n);
+    uint32_t* ticket = at<uint32_t>(ws, L.ticket);
+    MOE_LAUNCH("balance_partial", s,
+               if (launch_ex(balance_partial_kernel, nwin, 256, 0, s, pdl_enabled(), logits, bias,
+                             topk_idx, token_mask, seq_offsets, static_cast<int>(n_seq), p->T,
+                             p->E, p->top_k, win, part_p, part_c, part_n, ticket, status) !=
+                   cudaSuccess) return MOE_ERR_CUDA);
+    MOE_LAUNCH("balance_final", s,
+               if (launch_ex(balance_final_kernel, n_seq, kBalGroups * kMaxExperts, 0, s,
+                             pdl_enabled(), static_cast<const float*>(part_p),
+                             static_cast<const int32_t*>(part_c),
+                             static_cast<const int32_t*>(part_n), seq_offsets,
+                             static_cast<int>(n_seq), p->T, p->E, p->top_k, win, mean_prob, counts,
+                             tokens, at<double>(ws, L.seq_loss), ticket, loss, status) !=
+                   cudaSuccess) return MOE_ERR_CUDA);
+    return MOE_OK;
+}
+
+int32_t moe_balance_loss_backward(const moe_problem* p, const float* logits, const float* bias,
+                                  const uint8_t* token_mask, const int32_t* seq_offsets,
+                                  int32_t n_seq, const int32_t* counts, const int32_t* tokens,
+                                  const float* grad_loss, float* dlogits, void* stream) {
+    MOE_TRY(check_problem(p));
+    MOE_TRY(check_sequences(seq_offsets, n_seq));
+    if (!logits || !counts || !tokens || !grad_loss || !dlogits) return MOE_ERR_INVALID_ARG;
+    if (p->T == 0) return MOE_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // consecutive tokens per warp: about 32 warps per SM
+    const int64_t warps = 148 * 32;
+    const int run = static_cast<int>((p->T + warps - 1) / warps);
+    const int grid = static_cast<int>((p->T + 8 * run - 1) / (8 * run));
+    MOE_LAUNCH("balance_backward", s,
+               if (launch_ex(balance_backward_kernel, grid, 256, 0, s, pdl_enabled(), logits, bias,
+                             token_mask, seq_offsets, static_cast<int>(n_seq), p->T, p->E,
+                             p->top_k, run, counts, tokens, grad_loss, dlogits) != cudaSuccess)
+                   return MOE_ERR_CUDA);
+    return MOE_OK;
+}
+
+int32_t moe_quantize_weights_w4(const moe_problem* p, int32_t group_size, int32_t n_experts,
+                                const void* w, uint8_t* q, void* scales, void* stream) {
+    MOE_TRY(check_w4(p, group_size));
+    if (!w || !q || !scales) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(w) || !aligned16(q) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+    if (n_experts < 1 || n_experts > 65535) return MOE_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const dim3 grid(static_cast<unsigned>(3ll * p->I * p->H / (16 * kW4Block)),
+                    static_cast<unsigned>(n_experts));
+    __nv_bfloat16* sc = static_cast<__nv_bfloat16*>(scales);
+    auto go = [&](auto* in) -> int32_t {
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(in)>>;
+        auto kern = group_size == 128 ? w4_encode_kernel<T, 1>
+                                      : (group_size == 64 ? w4_encode_kernel<T, 2>
+                                                          : w4_encode_kernel<T, 4>);
+        MOE_LAUNCH("quantize_weights_w4", s, kern<<<grid, 128, 0, s>>>(in, p->I, p->H, q, sc));
+        return MOE_OK;
+    };
+    if (p->dtype == MOE_BF16) return go(static_cast<const __nv_bfloat16*>(w));
+    return go(static_cast<const float*>(w));
+}
+
+int32_t moe_experts_w4(const moe_problem* p, int32_t group_size, const void* x,
+                       const int32_t* topk_idx, const float* topk_w, const uint8_t* expert_q,
+                       const void* expert_scale, const uint8_t* shared_q,
+                       const void* shared_scale, void* out, void* ws, size_t ws_bytes,
+                       void* stream) {
+    MOE_TRY(check_w4_call(p, group_size, x, expert_q, expert_scale, shared_q, shared_scale, out,
+                          ws));
+    if (!topk_idx || !topk_w) return MOE_ERR_INVALID_ARG;
+    const W4Layout L = w4_layout(p, false);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    if (p->T == 0) return MOE_OK;
+    return run_experts_w4(p, group_size, x, topk_idx, topk_w, expert_q, expert_scale, shared_q,
+                          shared_scale, out, ws, L, static_cast<cudaStream_t>(stream));
+}
+
+int32_t moe_forward_w4(const moe_problem* p, int32_t group_size, const void* x,
+                       const void* gate_w, const float* bias, const uint8_t* expert_q,
+                       const void* expert_scale, const uint8_t* shared_q,
+                       const void* shared_scale, void* out, int32_t* idx_out, float* w_out,
+                       void* ws, size_t ws_bytes, void* stream) {
+    MOE_TRY(check_w4_call(p, group_size, x, expert_q, expert_scale, shared_q, shared_scale, out,
+                          ws));
+    if (!gate_w || !aligned16(gate_w)) return MOE_ERR_INVALID_ARG;
+    const W4Layout L = w4_layout(p, true);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    if (p->T == 0) return MOE_OK;
+    int32_t* idx = idx_out ? idx_out : at<int32_t>(ws, L.idx);
+    float* w = w_out ? w_out : at<float>(ws, L.w);
+    MOE_TRY(moe_route(p, x, gate_w, bias, idx, w, ws, ws_bytes, stream));
+    return run_experts_w4(p, group_size, x, idx, w, expert_q, expert_scale, shared_q, shared_scale,
+                          out, ws, L, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -11,9 +11,6 @@
 
 namespace moe {
 
-constexpr int kPermTokens = 256;  // tokens per dispatch chunk (one CTA, 8 warps)
-constexpr int kPermWarps = kPermTokens / 32;
-
 // ------------------------------------------------------------------ routing
 
 // Router logits in fp32 for fp32 inputs: logits[t,e] = sum_h x[t,h] * w[e,h].
@@ -142,26 +139,6 @@ __global__ void router_stats_final_kernel(const float* __restrict__ partial, int
 
 // ------------------------------------------------------------------ dispatch
 
-// Build, for the warp's 32 tokens, one bit mask per expert of the lanes whose
-// token routes to it.  A token's k experts must be distinct; a repeat, or an
-// index outside [0,E), is reported through `status` and skipped.
-__device__ __forceinline__ void build_lane_masks(const int32_t* __restrict__ idx, int64_t T, int E,
-                                                 int k, int64_t t, uint32_t* warp_masks,
-                                                 int32_t* status) {
-    const int lane = threadIdx.x & 31;
-    if (t < T) {
-        for (int j = 0; j < k; ++j) {
-            const int e = idx[t * k + j];
-            if (e < 0 || e >= E) {
-                set_device_error(status, DEV_ERR_BAD_INDEX);
-                continue;
-            }
-            const uint32_t old = atomicOr(&warp_masks[e], 1u << lane);
-            if (old & (1u << lane)) set_device_error(status, DEV_ERR_BAD_INDEX);
-        }
-    }
-}
-
 // Pass 1: per-chunk expert histogram hist[chunk, e].
 __global__ void dispatch_count_kernel(const int32_t* __restrict__ idx, int64_t T, int E, int k,
                                       int32_t* __restrict__ hist, int32_t* status) {
@@ -179,35 +156,6 @@ __global__ void dispatch_count_kernel(const int32_t* __restrict__ idx, int64_t T
         for (int w = 0; w < kPermWarps; ++w) c += __popc(masks[w][e]);
         hist[static_cast<size_t>(blockIdx.x) * E + e] = c;
     }
-}
-
-// Exclusive prefix sum over the CTA (blockDim.x a multiple of 32, <= 1024).
-// `s_warp` is 32 ints of shared scratch; every thread must call it.
-__device__ __forceinline__ int block_exclusive_scan(int v, int* s_warp, int* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nwarps = blockDim.x >> 5;
-    int x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int w = lane < nwarps ? s_warp[lane] : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += y;
-        }
-        s_warp[lane] = w;
-    }
-    __syncthreads();
-    const int result = (warp > 0 ? s_warp[warp - 1] : 0) + x - v;
-    if (total) *total = s_warp[nwarps - 1];
-    __syncthreads();
-    return result;
 }
 
 // Tile schedule entry of one segment (see SchedPtrs): chunk count and chunk
@@ -561,14 +509,6 @@ __global__ void wait_selftest_kernel(const int32_t* counter, uint64_t limit_cycl
 // v / s is exact and the E4M3 code of v / s does not depend on the precision
 // the division is done in.
 
-__device__ __forceinline__ float pow2_scale_f(float amax) {
-    if (!(amax > 0.0f)) return 1.0f;
-    int n = ilogbf(amax) - 8;  // 2^8 < 448 < 2^9
-    while (ldexpf(448.0f, n) < amax) ++n;
-    while (n > -126 && ldexpf(448.0f, n - 1) >= amax) --n;
-    return ldexpf(1.0f, n);
-}
-
 template <typename T>
 __device__ __forceinline__ float load_f32(const T* p, int64_t i);
 template <>
@@ -588,24 +528,6 @@ __device__ __forceinline__ float load_f32<__nv_bfloat16>(const __nv_bfloat16* p,
 // len is a multiple of 128 (so rows are 16-byte aligned): each lane reads
 // 16-byte vectors (8 bf16 or 4 fp32 values), eight in flight, and writes each
 // vector's codes at once.
-template <typename T>
-__device__ __forceinline__ void unpack_vec(const uint4& q, float (&f)[16 / sizeof(T)]) {
-    if constexpr (sizeof(T) == 2) {
-        const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 v = __bfloat1622float2(h2[e]);
-            f[2 * e] = v.x;
-            f[2 * e + 1] = v.y;
-        }
-    } else {
-        f[0] = __uint_as_float(q.x);
-        f[1] = __uint_as_float(q.y);
-        f[2] = __uint_as_float(q.z);
-        f[3] = __uint_as_float(q.w);
-    }
-}
-
 template <typename T>
 __global__ void quantize_rows_e4m3_kernel(const T* __restrict__ in, int64_t n_rows, int len,
                                           int64_t group, int64_t src_group_stride,

@@ -27,14 +27,19 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, 1, 2, 3
 MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_BAD_INDEX = 4, 5, 6
 MOE_F32, MOE_BF16 = 0, 1
 (MOE_CALL_ROUTE, MOE_CALL_ROUTER_LOGITS, MOE_CALL_PERMUTE, MOE_CALL_FFN, MOE_CALL_COMBINE,
- MOE_CALL_FORWARD, MOE_CALL_ROUTER_STATS, MOE_CALL_FORWARD_FP8) = range(8)
+ MOE_CALL_FORWARD, MOE_CALL_ROUTER_STATS, MOE_CALL_FORWARD_FP8,
+ MOE_CALL_ADD_RMSNORM_BACKWARD, MOE_CALL_BALANCE_LOSS, MOE_CALL_EXPERTS_W4,
+ MOE_CALL_FORWARD_W4) = range(12)
 
 EXPORTED = (
     "moe_workspace_size", "moe_status_string", "moe_router_logits", "moe_route", "moe_permute",
     "moe_grouped_swiglu_ffn", "moe_combine", "moe_forward", "moe_read_device_status",
     "moe_clear_device_status", "moe_launch_count", "moe_profile_start", "moe_profile_stop",
     "moe_route_noalloc", "moe_router_stats", "moe_quantize_weights_fp8", "moe_forward_fp8",
-    "moe_check_wait_timeout", "moe_expert_tile_rows",
+    "moe_check_wait_timeout", "moe_expert_tile_rows", "moe_forward_fp8_encoded",
+    "moe_add_rmsnorm", "moe_add_rmsnorm_backward", "moe_balance_loss_workspace_size",
+    "moe_balance_loss", "moe_balance_loss_backward", "moe_quantize_weights_w4", "moe_experts_w4",
+    "moe_forward_w4",
 )
 ROUTE_NOALLOC_SCRATCH_BYTES = 1 << 20
 
@@ -120,6 +125,16 @@ def load_library(path: str = LIB_PATH):
             "moe_forward_fp8": (I32, [PP, P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
             "moe_check_wait_timeout": (I32, [P, SZ, ctypes.POINTER(I32), P]),
             "moe_expert_tile_rows": (I32, [PP, ctypes.POINTER(I32), ctypes.POINTER(I32)]),
+            "moe_forward_fp8_encoded": (I32, [PP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, SZ,
+                                              P]),
+            "moe_add_rmsnorm": (I32, [PP, P, P, P, ctypes.c_float, P, P, P, P, P]),
+            "moe_add_rmsnorm_backward": (I32, [PP, P, P, P, P, ctypes.c_float, P, P, P, SZ, P]),
+            "moe_balance_loss_workspace_size": (SZ, [PP, I32]),
+            "moe_balance_loss": (I32, [PP, P, P, P, P, P, I32, P, P, P, P, P, SZ, P]),
+            "moe_balance_loss_backward": (I32, [PP, P, P, P, P, I32, P, P, P, P, P]),
+            "moe_quantize_weights_w4": (I32, [PP, I32, I32, P, P, P, P]),
+            "moe_experts_w4": (I32, [PP, I32, P, P, P, P, P, P, P, P, P, SZ, P]),
+            "moe_forward_w4": (I32, [PP, I32, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -183,6 +198,31 @@ def _spec(t, dtype=None, name="tensor", optional=False, numel=None):
 def _check(status: int, what: str):
     if status != MOE_OK:
         raise MoEError(status, what)
+
+
+def _run(name, problem, before, operands, workspace, stream):
+    """Call entry point `name` with the problem, the plain values `before`, the
+    operands (specs, checked as _ptrs checks them, and plain values between
+    them), the workspace and its size (if there is one) and the stream.  The
+    operands lie on one device; the call is made with that device current, on
+    its current stream unless `stream` names one."""
+    specs = [o for o in operands if type(o) is tuple]
+    if workspace is not None:
+        specs.append(_ws(workspace))
+    ptrs = iter(_ptrs(*specs))
+    device = specs[0][0].device
+    for s in specs:
+        if s[0] is not None and s[0].device != device:
+            raise ValueError(f"{s[2]} is on {s[0].device}, {specs[0][2]} on {device}")
+    args = [next(ptrs) if type(o) is tuple else o for o in operands]
+    if workspace is not None:
+        args += [next(ptrs), workspace.numel() * workspace.element_size()]
+    pc = problem.c()
+    with torch.cuda.device(device):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        _check(getattr(load_library(), name)(ctypes.byref(pc), *before, *args, _stream(stream)),
+               name)
 
 
 def moe_workspace_size(problem: MoEProblem, call: int) -> int:
@@ -293,6 +333,158 @@ def moe_forward_fp8(problem, x, gate_w, logit_bias, expert_q, expert_s_gu, exper
                  _ws(workspace))
     _check(load_library().moe_forward_fp8(ctypes.byref(pc), *ptrs, workspace.numel(),
                                           _stream(stream)), "moe_forward_fp8")
+
+
+def moe_forward_fp8_encoded(problem, x, x_q, x_scale, gate_w, logit_bias, expert_q, expert_s_gu,
+                            expert_s_d, shared_q, shared_s_gu, shared_s_d, out, topk_idx_out,
+                            topk_w_out, workspace, stream=None):
+    """moe_forward_fp8 on rows encoded already (y_q and y_scale of moe_add_rmsnorm)."""
+    T, H, E, I, k = problem.T, problem.H, problem.E, problem.I, problem.top_k
+    _run("moe_forward_fp8_encoded", problem, (), (
+        _spec(x, torch.bfloat16, "x", numel=T * H),
+        _spec(x_q, torch.uint8, "x_q", numel=T * H),
+        _spec(x_scale, torch.float32, "x_scale", numel=T),
+        _spec(gate_w, torch.bfloat16, "gate_w", numel=E * H),
+        _spec(logit_bias, torch.float32, "logit_bias", optional=True, numel=E),
+        _spec(expert_q, torch.uint8, "expert_q", numel=E * 3 * I * H),
+        _spec(expert_s_gu, torch.float32, "expert_s_gu", numel=E * 2 * I),
+        _spec(expert_s_d, torch.float32, "expert_s_d", numel=E * H),
+        _spec(shared_q, torch.uint8, "shared_q", optional=True, numel=3 * I * H),
+        _spec(shared_s_gu, torch.float32, "shared_s_gu", optional=True, numel=2 * I),
+        _spec(shared_s_d, torch.float32, "shared_s_d", optional=True, numel=H),
+        _spec(out, torch.bfloat16, "out", numel=T * H),
+        _spec(topk_idx_out, torch.int32, "topk_idx_out", optional=True, numel=T * k),
+        _spec(topk_w_out, torch.float32, "topk_w_out", optional=True, numel=T * k)),
+        workspace, stream)
+
+
+def moe_add_rmsnorm(problem, x, residual, weight, eps, residual_out, y, y_q=None, y_scale=None,
+                    stream=None):
+    """Residual addition and RMS norm of the layer's rows, optionally with the
+    E4M3 codes and scales that moe_forward_fp8_encoded takes."""
+    T, H, dt = problem.T, problem.H, problem.dtype
+    _run("moe_add_rmsnorm", problem, (), (
+        _spec(x, dt, "x", numel=T * H),
+        _spec(residual, dt, "residual", optional=True, numel=T * H),
+        _spec(weight, dt, "weight", numel=H), float(eps),
+        _spec(residual_out, dt, "residual_out", optional=True, numel=T * H),
+        _spec(y, dt, "y", optional=True, numel=T * H),
+        _spec(y_q, torch.uint8, "y_q", optional=True, numel=T * H),
+        _spec(y_scale, torch.float32, "y_scale", optional=True, numel=T)), None, stream)
+
+
+def moe_add_rmsnorm_backward(problem, dy, dresidual, h, weight, eps, dx, dweight, workspace,
+                             stream=None):
+    """Gradients of moe_add_rmsnorm; h is its residual_out."""
+    T, H, dt = problem.T, problem.H, problem.dtype
+    _run("moe_add_rmsnorm_backward", problem, (), (
+        _spec(dy, dt, "dy", numel=T * H),
+        _spec(dresidual, dt, "dresidual", optional=True, numel=T * H),
+        _spec(h, dt, "h", numel=T * H), _spec(weight, dt, "weight", numel=H), float(eps),
+        _spec(dx, dt, "dx", numel=T * H),
+        _spec(dweight, torch.float32, "dweight", numel=H)), workspace, stream)
+
+
+def _sequences(seq_offsets):
+    """Number of sequences that the offsets describe (None: the whole batch is one)."""
+    if seq_offsets is None:
+        return 1
+    if not isinstance(seq_offsets, torch.Tensor) or seq_offsets.dim() != 1:
+        raise ValueError("seq_offsets must be a tensor of n_seq + 1 offsets")
+    return seq_offsets.shape[0] - 1
+
+
+def moe_balance_loss_workspace_size(problem: MoEProblem, n_seq: int) -> int:
+    pc = problem.c()
+    return int(load_library().moe_balance_loss_workspace_size(ctypes.byref(pc), int(n_seq)))
+
+
+def alloc_balance_workspace(problem: MoEProblem, n_seq: int = 1, device=None) -> torch.Tensor:
+    """Caller-owned workspace for moe_balance_loss over n_seq sequences; plumbing only."""
+    n = moe_balance_loss_workspace_size(problem, n_seq)
+    if n == 0:
+        raise MoEError(MOE_ERR_UNSUPPORTED, "moe_balance_loss_workspace_size")
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws[:256].zero_()
+    return ws
+
+
+def moe_balance_loss(problem, logits, logit_bias, topk_idx, token_mask, seq_offsets, loss, counts,
+                     tokens, mean_prob, workspace, stream=None):
+    """Balance loss of the router over packed sequences, with the counts and
+    token counts that its backward call takes."""
+    T, E, k, n = problem.T, problem.E, problem.top_k, _sequences(seq_offsets)
+    _run("moe_balance_loss", problem, (), (
+        _spec(logits, torch.float32, "logits", numel=T * E),
+        _spec(logit_bias, torch.float32, "logit_bias", optional=True, numel=E),
+        _spec(topk_idx, torch.int32, "topk_idx", numel=T * k),
+        _spec(token_mask, torch.uint8, "token_mask", optional=True, numel=T),
+        _spec(seq_offsets, torch.int32, "seq_offsets", optional=True, numel=n + 1), n,
+        _spec(loss, torch.float32, "loss", numel=1),
+        _spec(counts, torch.int32, "counts", numel=n * E),
+        _spec(tokens, torch.int32, "tokens", numel=n + 1),
+        _spec(mean_prob, torch.float32, "mean_prob", numel=n * E)), workspace, stream)
+
+
+def moe_balance_loss_backward(problem, logits, logit_bias, token_mask, seq_offsets, counts, tokens,
+                              grad_loss, dlogits, stream=None):
+    """Gradient of moe_balance_loss with respect to the logits."""
+    T, E, n = problem.T, problem.E, _sequences(seq_offsets)
+    _run("moe_balance_loss_backward", problem, (), (
+        _spec(logits, torch.float32, "logits", numel=T * E),
+        _spec(logit_bias, torch.float32, "logit_bias", optional=True, numel=E),
+        _spec(token_mask, torch.uint8, "token_mask", optional=True, numel=T),
+        _spec(seq_offsets, torch.int32, "seq_offsets", optional=True, numel=n + 1), n,
+        _spec(counts, torch.int32, "counts", numel=n * E),
+        _spec(tokens, torch.int32, "tokens", numel=n + 1),
+        _spec(grad_loss, torch.float32, "grad_loss", numel=1),
+        _spec(dlogits, torch.float32, "dlogits", numel=T * E)), None, stream)
+
+
+def moe_quantize_weights_w4(problem, group_size, w, q, scales, stream=None):
+    """Encode [n,3,I,H] weights into packed 4-bit codes q (uint8, n*3*I*H/2
+    bytes) and bf16 scales (n*3*I*H/group_size); n is w.shape[0]."""
+    n, g, per = int(w.shape[0]), int(group_size), 3 * problem.I * problem.H
+    _run("moe_quantize_weights_w4", problem, (g, n), (
+        _spec(w, problem.dtype, "w", numel=n * per),
+        _spec(q, torch.uint8, "q", numel=n * per // 2),
+        _spec(scales, torch.bfloat16, "scales", numel=n * per // max(1, g))), None, stream)
+
+
+def _w4_specs(problem, g, expert_q, expert_scale, shared_q, shared_scale, out):
+    T, H, E, per = problem.T, problem.H, problem.E, 3 * problem.I * problem.H
+    return (_spec(expert_q, torch.uint8, "expert_q", numel=E * per // 2),
+            _spec(expert_scale, torch.bfloat16, "expert_scale", numel=E * per // max(1, g)),
+            _spec(shared_q, torch.uint8, "shared_q", optional=True, numel=per // 2),
+            _spec(shared_scale, torch.bfloat16, "shared_scale", optional=True,
+                  numel=per // max(1, g)),
+            _spec(out, torch.bfloat16, "out", numel=T * H))
+
+
+def moe_experts_w4(problem, group_size, x, topk_idx, topk_w, expert_q, expert_scale, shared_q,
+                   shared_scale, out, workspace, stream=None):
+    """The layer behind its router with 4-bit expert weights."""
+    T, H, k, g = problem.T, problem.H, problem.top_k, int(group_size)
+    _run("moe_experts_w4", problem, (g,), (
+        _spec(x, torch.bfloat16, "x", numel=T * H),
+        _spec(topk_idx, torch.int32, "topk_idx", numel=T * k),
+        _spec(topk_w, torch.float32, "topk_w", numel=T * k),
+        *_w4_specs(problem, g, expert_q, expert_scale, shared_q, shared_scale, out)),
+        workspace, stream)
+
+
+def moe_forward_w4(problem, group_size, x, gate_w, logit_bias, expert_q, expert_scale, shared_q,
+                   shared_scale, out, topk_idx_out, topk_w_out, workspace, stream=None):
+    """moe_route and moe_experts_w4 in one call."""
+    T, H, E, k, g = problem.T, problem.H, problem.E, problem.top_k, int(group_size)
+    _run("moe_forward_w4", problem, (g,), (
+        _spec(x, torch.bfloat16, "x", numel=T * H),
+        _spec(gate_w, torch.bfloat16, "gate_w", numel=E * H),
+        _spec(logit_bias, torch.float32, "logit_bias", optional=True, numel=E),
+        *_w4_specs(problem, g, expert_q, expert_scale, shared_q, shared_scale, out),
+        _spec(topk_idx_out, torch.int32, "topk_idx_out", optional=True, numel=T * k),
+        _spec(topk_w_out, torch.float32, "topk_w_out", optional=True, numel=T * k)),
+        workspace, stream)
 
 
 def moe_check_wait_timeout(workspace, stream=None) -> int:
