@@ -269,7 +269,7 @@ int32_t check_w4_call(const moe_problem* p, int32_t group, const void* x, const 
                       const void* ws) {
     MOE_TRY(check_w4(p, group));
     if (p->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
-    if (!x || !eq || !es || !out || !ws) return MOE_ERR_INVALID_ARG;
+    if (!eq || !es || !ws || (p->T > 0 && (!x || !out))) return MOE_ERR_INVALID_ARG;
     if (p->num_shared && (!sq || !ss)) return MOE_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(eq) || !aligned16(es) || !aligned16(out) || !aligned16(ws) ||
         (sq && !aligned16(sq)) || (ss && !aligned16(ss)))
@@ -305,7 +305,9 @@ int32_t moe_add_rmsnorm(const moe_problem* p, const void* x, const void* residua
                         const void* weight, float eps, void* residual_out, void* y, uint8_t* y_q,
                         float* y_scale, void* stream) {
     MOE_TRY(check_norm(p, eps));
-    if (!x || !weight || (!y && !y_q) || (!y_q) != (!y_scale)) return MOE_ERR_INVALID_ARG;
+    if (!weight) return MOE_ERR_INVALID_ARG;
+    // (an empty batch's row pointers may be null)
+    if (p->T > 0 && (!x || (!y && !y_q) || (!y_q) != (!y_scale))) return MOE_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) ||
         !aligned16(y) || !aligned16(y_q))
         return MOE_ERR_INVALID_ARG;
@@ -321,7 +323,7 @@ int32_t moe_add_rmsnorm_backward(const moe_problem* p, const void* dy, const voi
                                  const void* h, const void* weight, float eps, void* dx,
                                  float* dweight, void* ws, size_t ws_bytes, void* stream) {
     MOE_TRY(check_norm(p, eps));
-    if (!dy || !h || !weight || !dx || !dweight || !ws) return MOE_ERR_INVALID_ARG;
+    if (!weight || !dweight || !ws || (p->T > 0 && (!dy || !h || !dx))) return MOE_ERR_INVALID_ARG;
     if (!aligned16(dy) || !aligned16(dresidual) || !aligned16(h) || !aligned16(weight) ||
         !aligned16(dx) || !aligned16(ws))
         return MOE_ERR_INVALID_ARG;
@@ -352,7 +354,7 @@ int32_t moe_balance_loss(const moe_problem* p, const float* logits, const float*
                          void* stream) {
     MOE_TRY(check_problem(p));
     MOE_TRY(check_sequences(seq_offsets, n_seq));
-    if (!logits || !topk_idx || !loss || !counts || !tokens || !mean_prob || !ws)
+    if ((p->T > 0 && (!logits || !topk_idx)) || !loss || !counts || !tokens || !mean_prob || !ws)
         return MOE_ERR_INVALID_ARG;
     if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
     const BalanceLayout L = balance_layout(p, n_seq);
@@ -387,8 +389,8 @@ int32_t moe_balance_loss_backward(const moe_problem* p, const float* logits, con
                                   const float* grad_loss, float* dlogits, void* stream) {
     MOE_TRY(check_problem(p));
     MOE_TRY(check_sequences(seq_offsets, n_seq));
-    if (!logits || !counts || !tokens || !grad_loss || !dlogits) return MOE_ERR_INVALID_ARG;
     if (p->T == 0) return MOE_OK;
+    if (!logits || !counts || !tokens || !grad_loss || !dlogits) return MOE_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // consecutive tokens per warp: about 32 warps per SM
     const int64_t warps = 148 * 32;
@@ -431,7 +433,7 @@ int32_t moe_experts_w4(const moe_problem* p, int32_t group_size, const void* x,
                        void* stream) {
     MOE_TRY(check_w4_call(p, group_size, x, expert_q, expert_scale, shared_q, shared_scale, out,
                           ws));
-    if (!topk_idx || !topk_w) return MOE_ERR_INVALID_ARG;
+    if (p->T > 0 && (!topk_idx || !topk_w)) return MOE_ERR_INVALID_ARG;
     const W4Layout L = w4_layout(p, false);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     if (p->T == 0) return MOE_OK;
