@@ -120,7 +120,7 @@ int32_t check_w4(const moe_problem* p, int32_t group) {
 
 struct W4Layout {
     size_t status, route, idx, w, hist, base, counts, offsets, sched_gu, sched_dn, pos, src,
-        row_w, h, y, total;
+        row_w, x_rows, h, h_rows, y, total;
 };
 
 W4Layout w4_layout(const moe_problem* p, bool with_route) {
@@ -142,7 +142,9 @@ W4Layout w4_layout(const moe_problem* p, bool with_route) {
     L.pos = c.take(T * k * 4);
     L.src = c.take(T * k * 4);
     L.row_w = c.take(T * k * 4);
-    L.h = c.take(T * (k + S) * I * 4);  // bf16 high and low parts
+    L.x_rows = c.take(T * (H / kW4Block) * kW4RowBlock);
+    L.h = c.take(T * (k + S) * I * 4);
+    L.h_rows = c.take(T * (k + S) * (I / kW4Block) * kW4RowBlock);
     L.y = c.take(T * (k + S) * H * 4);
     L.total = c.off;
     return L;
@@ -162,19 +164,20 @@ int32_t launch_w4_n(const W4Args& a, int64_t max_tasks, cudaStream_t s) {
     cudaGetDevice(&dev);
     static std::atomic<int> per_sm[64];
     int n = dev < 64 ? per_sm[dev].load() : 0;
+    constexpr int smem = 2 * kW4Warps * 2 * NT * 128 * 4;  // two buffers of partial sums
     if (n == 0) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kW4Threads, 0) !=
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+                cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kW4Threads, smem) !=
                 cudaSuccess ||
             n < 1)
             return MOE_ERR_CUDA;
         if (dev < 64) per_sm[dev].store(n);
     }
-    const int64_t warps = kW4Threads / 32;
-    const int grid = static_cast<int>(
-        std::max<int64_t>(1, std::min<int64_t>(static_cast<int64_t>(sm_count()) * n,
-                                               (max_tasks + warps - 1) / warps)));
+    const int grid = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>(static_cast<int64_t>(sm_count()) * n, max_tasks)));
     MOE_LAUNCH(DOWN ? "expert_down_w4" : "expert_gate_up_w4", s,
-               if (launch_ex(kern, grid, kW4Threads, 0, s, pdl_enabled(), a) != cudaSuccess)
+               if (launch_ex(kern, grid, kW4Threads, smem, s, pdl_enabled(), a) != cudaSuccess)
                    return MOE_ERR_CUDA);
     return MOE_OK;
 }
@@ -208,11 +211,16 @@ int32_t run_experts_w4(const moe_problem* p, int32_t group, const void* x, const
     float* row_w = at<float>(ws, L.row_w);
     const int nt = w4_column_tiles(static_cast<double>(T * k) / E);
     const bool pdl = pdl_enabled();
+    const int sub = kW4Block / group;
+    const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
+    uint8_t* x_rows = at<uint8_t>(ws, L.x_rows);
+    const int64_t x_units = T * (H / kW4Block);
     if (T <= kPermTokens) {
         MOE_LAUNCH("dispatch_w4", s,
-                   if (launch_ex(w4_dispatch_kernel, 1, 512, 0, s, pdl, idx, w,
-                                 static_cast<int>(T), p->E, p->top_k, p->num_shared, 8 * nt, sg,
-                                 sd, pos, src, row_w, status) != cudaSuccess)
+                   if (launch_ex(w4_dispatch_kernel, 1 + static_cast<int>((x_units + 15) / 16),
+                                 512, 0, s, pdl, idx, w, static_cast<int>(T), p->E, p->top_k,
+                                 p->num_shared, 8 * nt, sg, sd, pos, src, row_w, status, xb,
+                                 x_units, sub, x_rows) != cudaSuccess)
                        return MOE_ERR_CUDA);
     } else {
         // (an assignment with an expert out of range keeps position -1)
@@ -221,6 +229,10 @@ int32_t run_experts_w4(const moe_problem* p, int32_t group, const void* x, const
         MOE_TRY(dispatch_rows(p, idx, w, at<int32_t>(ws, L.hist), at<int32_t>(ws, L.base),
                               at<int32_t>(ws, L.counts), at<int32_t>(ws, L.offsets), sg, 8 * nt,
                               sd, 8 * nt, pos, src, row_w, status, s));
+        MOE_LAUNCH("split_rows_w4", s,
+                   if (launch_ex(w4_split_kernel<__nv_bfloat16>,
+                                 static_cast<int>((x_units + 7) / 8), 256, 0, s, pdl, xb, x_units,
+                                 sub, x_rows) != cudaSuccess) return MOE_ERR_CUDA);
     }
     const int nseg = static_cast<int>(E + S);
     // at most this many chunks of 8 nt rows over all segments
@@ -240,21 +252,27 @@ int32_t run_experts_w4(const moe_problem* p, int32_t group, const void* x, const
     a.q_shared = sq;
     a.sc_shared = static_cast<const __nv_bfloat16*>(ss);
     a.sched = sg;
-    a.rows = static_cast<const __nv_bfloat16*>(x);
+    a.rows = x_rows;
     a.K = static_cast<int32_t>(H);
     a.tiles = static_cast<int32_t>(I / 16);
-    a.out = at<void>(ws, L.h);
+    a.out = at<float>(ws, L.h);
     a.ld = static_cast<int32_t>(I);
     MOE_TRY(launch_w4<false>(nt, group, a, chunks * a.tiles, s));
+    const int64_t h_units = T * (k + S) * (I / kW4Block);
+    uint8_t* h_rows = at<uint8_t>(ws, L.h_rows);
+    MOE_LAUNCH("split_h_w4", s,
+               if (launch_ex(w4_split_kernel<float>, static_cast<int>((h_units + 7) / 8), 256, 0,
+                             s, pdl, static_cast<const float*>(a.out), h_units, sub, h_rows) !=
+                   cudaSuccess) return MOE_ERR_CUDA);
     a.q = eq + I * H;
     a.sc = static_cast<const __nv_bfloat16*>(es) + 2 * I * H / group;
     a.q_shared = sq ? sq + I * H : nullptr;
     a.sc_shared = ss ? static_cast<const __nv_bfloat16*>(ss) + 2 * I * H / group : nullptr;
     a.sched = sd;
-    a.rows = at<__nv_bfloat16>(ws, L.h);
+    a.rows = h_rows;
     a.K = static_cast<int32_t>(I);
     a.tiles = static_cast<int32_t>(H / 32);
-    a.out = at<void>(ws, L.y);
+    a.out = at<float>(ws, L.y);
     a.ld = static_cast<int32_t>(H);
     MOE_TRY(launch_w4<true>(nt, group, a, chunks * a.tiles, s));
     return combine_rows_f32(p, at<float>(ws, L.y), pos, static_cast<__nv_bfloat16*>(out), status,

@@ -1,11 +1,21 @@
 // w4_kernels.cuh -- the experts' products with 4-bit weights and group scales.
 //
 // A weight is w = (u - 8) * s: u its 4-bit code, s the bf16 scale of its group
-// of G (32, 64 or 128) consecutive weights along the contraction.  Products
-// run on m16n8k16 bf16 MMAs with the weights as the 16-row operand, unpacked
-// in registers, and the token rows as the 8 columns: u - 8 is exact in bf16,
-// so a group's sum of (u - 8) * x carries fp32 rounding only; it is scaled and
-// added to the fp32 total once per group.
+// of G (32, 64 or 128) consecutive weights along the contraction.
+//
+// The products run on m16n8k32 integer MMAs (u8 codes x s8 limbs, exact s32
+// sums).  A mask of a packed word is an A register as it stands, the low nibbles
+// u of one row or the high ones, 16 u, of another: two ALU steps for 8 codes (a
+// bf16 fragment takes 7, and ran the first form of these kernels into the ALU
+// pipe, which has half rate).  A token row is split, per block of 128 values,
+// into a power-of-two scale a and 16-bit integers v = 256 hi + lo with two s8
+// limbs: bf16 values down to 2^-7 of the block's largest are exact, smaller ones
+// off by at most a / 2, 2^-15 of the largest, far inside the bf16 output's
+// rounding.  With the sums of the limbs of each group,
+//   sum_k (u_k - 8) s x_k = s a (256 (sum u hi - 8 sum hi) + (sum u lo - 8 sum lo)),
+// and an accumulator that starts from the bits of 1.5 * 2^23 less 8 times the
+// limb sum ends as the fp32 number 1.5 * 2^23 + sum (u - 8) limb: the result is
+// below 2^22, so no conversion is needed.
 //
 // Layout.  Each matrix (gate/up: rows i of both, contraction H; down: rows h,
 // contraction I) is cut into pair tiles of 2 x 16 rows (gate/up: 16 gate rows
@@ -15,9 +25,11 @@
 // 16 x 128 half of a block is 1 KB, 32 bytes (one load) for each of 32 lanes:
 // lane 4r + c holds rows r (low nibble of each byte) and r + 8 (high nibble),
 // word 2a + b of its 8 the k = 32 a + 8 c + 4 b + {0, 2, 1, 3} (one per byte):
-// the A fragment of one MMA, a nibble of each half word per register.
-// The matching B fragments of two MMAs are 8 consecutive values of a token row
-// (one 16-byte load).  Scales: [tile][block][r 8][128/G][half][r, r + 8] bf16.
+// with both words of a, the A fragments of one MMA.
+// Scales: [tile][block][r 8][128/G][half][r, r + 8] bf16.
+// Limbs of a row and block: [a / 2][limb][c 4][a % 2][8 bytes], the 8 bytes in
+// the order of the two words; behind them the limb sums of each group (two
+// int16) and the scale, in 32 bytes.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -31,6 +43,7 @@ namespace moe {
 constexpr int kW4Block = 128;       // contraction length of a block
 constexpr int kW4BlockBytes = 2048; // codes of a pair tile's block
 constexpr int kW4Threads = 256;
+constexpr int kW4Warps = kW4Threads / 32;
 
 struct W4Args {
     const uint8_t* q;          // codes of expert 0's matrix
@@ -40,15 +53,30 @@ struct W4Args {
     int64_t q_stride, sc_stride;  // bytes / scales from one expert to the next
     const int32_t* sched;      // tile schedule of nseg segments (chunk j: rows from j * 8 NT)
     int32_t nseg, special;
-    const __nv_bfloat16* rows; // token rows [*, K] (down: [*, K/8, {hi, lo}, 8])
+    const uint8_t* rows;       // row blocks of the token rows
     const int32_t* row_src;    // gate/up: token of each routed row (special: the row itself)
     int32_t K, tiles;          // contraction length, pair tiles
-    void* out;                 // gate/up: h rows as above; down: fp32 [*, ld]
+    float* out;                // gate/up: h rows, down: weighted rows; fp32 [*, ld]
     int32_t ld;
     const float* row_w;        // down: routing weight of each routed row
     int32_t routed_rows;       // rows from here on have weight 1
     float clip;
 };
+
+__device__ __forceinline__ void mma_u8s8(int32_t (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+constexpr int32_t kW4MagicBits = 0x4b400000;   // 1.5 * 2^23 as fp32
+constexpr float kW4Magic = 12582912.0f;
+
+// Bytes of a row's block: two limbs of 128 values, the group sums, the scale.
+constexpr int kW4RowBlock = 2 * kW4Block + 32;
 
 // 32 bytes that are read once: past L1, first to leave L2.
 __device__ __forceinline__ void ldg_stream(const void* p, uint32_t (&v)[8]) {
@@ -59,96 +87,201 @@ __device__ __forceinline__ void ldg_stream(const void* p, uint32_t (&v)[8]) {
         : "l"(p));
 }
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// The 8 codes of a word as the A fragment of one MMA: 0x4300 | u is the bf16
-// value 128 + u, and subtracting 136 leaves u - 8 exactly.
-__device__ __forceinline__ void w4_fragment(uint32_t w, uint32_t (&a)[4]) {
-    const __nv_bfloat162 off = __float2bfloat162_rn(136.0f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), off);
-        a[i] = *reinterpret_cast<const uint32_t*>(&d);
-    }
-}
-
 // The codes and scales of one block of a pair tile, as one lane holds them.
 template <int SUB>
 struct W4Stage {
-    uint32_t a[2][8];          // [half]: word 2 * k32 + MMA
-    __nv_bfloat162 s[SUB][2];  // [group][half]: scales of rows r and r + 8
+    uint32_t a[2][8];  // [half]: word 2 * k32 + j
+    uint2 s[SUB];      // [group]: half 0's and half 1's scales of rows r and r + 8
 };
 
-template <int SUB>
-__device__ __forceinline__ void w4_load(W4Stage<SUB>& st, const uint8_t* q,
-                                        const __nv_bfloat16* sc) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) ldg_stream(q + h * 1024, st.a[h]);
-    if constexpr (SUB == 1) {
-        *reinterpret_cast<uint2*>(&st.s[0][0]) = __ldg(reinterpret_cast<const uint2*>(sc));
+// Row block `unit` of rows in [*, K] order, by one warp: lane l has the values
+// 4 l .. 4 l + 3.  The scale is the power of two a with 16191 <= amax / a <=
+// 32384, which leaves both limbs of rint(x / a) in range (32640 would need 128).
+// A block with a value that is not finite gets a NaN scale, so its row's results
+// are NaN.
+template <typename T>
+__device__ __forceinline__ void w4_split_block(const T* __restrict__ rows, int sub, int64_t unit,
+                                               uint8_t* __restrict__ out) {
+    const int lane = threadIdx.x & 31;
+    float v[4];
+    const T* in = rows + unit * kW4Block + lane * 4;
+    if constexpr (sizeof(T) == 2) {
+        const uint2 q = *reinterpret_cast<const uint2*>(in);
+        const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q.x));
+        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q.y));
+        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
     } else {
-#pragma unroll
-        for (int u = 0; u < SUB; u += 2)
-            *reinterpret_cast<uint4*>(&st.s[u][0]) =
-                __ldg(reinterpret_cast<const uint4*>(sc + u * 4));
+        const float4 q = *reinterpret_cast<const float4*>(in);
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
     }
+    float amax = 0.0f;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        amax = fmaxf(amax, fabsf(v[i]));
+        bad |= !isfinite(v[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    bad = __any_sync(0xffffffffu, bad);
+    // amax = m * 2^e, 1 <= m < 2; a = 2^(e-14), twice that for m > 253/128.  a and
+    // 1 / a stay normal: blocks below 2^-112 keep an absolute step of 2^-127
+    const uint32_t bits = __float_as_uint(amax);
+    int n = static_cast<int>(bits >> 23) - 127 - 14 + ((bits & 0x7fffffu) > 0x7d0000u ? 1 : 0);
+    n = min(max(n, -126), 126);
+    const float scale = __uint_as_float(static_cast<uint32_t>(n + 127) << 23);
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - n) << 23);
+    out += unit * kW4RowBlock;
+    uint32_t* meta = reinterpret_cast<uint32_t*>(out + 2 * kW4Block);
+    out += (lane >> 4) * 128 + ((lane & 7) >> 1) * 16 + ((lane >> 3) & 1) * 8 + (lane & 1) * 4;
+    uint32_t hi = 0, lo = 0;
+    int sum_hi = 0, sum_lo = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = bad ? 0 : __float2int_rn(v[i] * inv);
+        const int l = static_cast<int8_t>(t & 0xff), h = (t - l) >> 8;
+        const int at = ((i & 1) << 1) | (i >> 1);  // bytes k, k + 2, k + 1, k + 3
+        hi |= static_cast<uint32_t>(h & 0xff) << (8 * at);
+        lo |= static_cast<uint32_t>(l & 0xff) << (8 * at);
+        sum_hi += h;
+        sum_lo += l;
+    }
+    *reinterpret_cast<uint32_t*>(out) = hi;
+    *reinterpret_cast<uint32_t*>(out + 64) = lo;
+    const int per = 32 / sub;  // lanes of a group
+    for (int o = 1; o < per; o <<= 1) {
+        sum_hi += __shfl_xor_sync(0xffffffffu, sum_hi, o);
+        sum_lo += __shfl_xor_sync(0xffffffffu, sum_lo, o);
+    }
+    if (lane % per == 0)
+        meta[lane / per] = (static_cast<uint32_t>(sum_hi) << 16) |
+                           (static_cast<uint32_t>(sum_lo) & 0xffffu);
+    if (lane == 0) meta[sub] = bad ? 0x7fc00000u : __float_as_uint(scale);
 }
 
-// One warp per task: a pair tile against up to 8 NT token rows of one segment,
-// over the whole contraction.  Tasks are numbered (segment, tile, chunk).
+template <typename T>
+__global__ void __launch_bounds__(256) w4_split_kernel(const T* __restrict__ rows, int64_t units,
+                                                       int sub, uint8_t* __restrict__ out) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (unit < units) w4_split_block<T>(rows, sub, unit, out);
+}
+
+// Where a CTA's next tile lies: its segment and chunk of token rows.
+struct W4Place {
+    int seg, tile, chunk, chunks;
+};
+
+// Task t of the launch, tasks numbered (segment, tile, chunk): the segment is
+// the last one whose first task is not behind t.
+__device__ __forceinline__ W4Place w4_place(const SchedPtrs& sp, int nseg, int tiles, int64_t t) {
+    int lo = 0, hi = nseg - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (static_cast<int64_t>(sp.prefix[mid]) * tiles <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    W4Place p;
+    p.seg = lo;
+    p.chunks = sp.prefix[lo + 1] - sp.prefix[lo];
+    const int in_seg = static_cast<int>(t - static_cast<int64_t>(sp.prefix[lo]) * tiles);
+    p.tile = in_seg / p.chunks;
+    p.chunk = in_seg - p.tile * p.chunks;
+    return p;
+}
+
+// The task behind p (if there is one: empty segments are passed over).
+__device__ __forceinline__ void w4_advance(W4Place& p, const SchedPtrs& sp, int nseg, int tiles) {
+    if (++p.chunk < p.chunks) return;
+    p.chunk = 0;
+    if (++p.tile < tiles) return;
+    p.tile = 0;
+    do {
+        ++p.seg;
+        p.chunks = p.seg < nseg ? sp.prefix[p.seg + 1] - sp.prefix[p.seg] : 1;
+    } while (p.chunks == 0);
+}
+
+// Warps that share a tile, for CTAs with `run` tiles each: one where that many
+// rounds keep every warp busy, else all that the contraction has blocks for.
+__device__ __forceinline__ int w4_ksplit(int64_t run, int nkb) {
+    const int most = nkb >= 8 ? 8 : (nkb >= 4 ? 4 : (nkb >= 2 ? 2 : 1));
+    return run >= 96 ? min(2, most) : most;
+}
+
+// A CTA takes a run of consecutive tasks, each a pair tile against up to 8 NT
+// token rows of one segment.  Its warps split the contraction: KS of them share
+// a tile (8 / KS tiles at a time), warp k of them taking the k-th part of the
+// blocks; their fp32 sums are added in shared memory in warp order.  The weights
+// stream through registers, two blocks ahead, past L1, which keeps the token
+// rows that the warps share.
 template <int NT, bool DOWN, int SUB>
-__global__ void __launch_bounds__(kW4Threads) w4_product_kernel(const W4Args args) {
-    const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1)
+    w4_product_kernel(const W4Args args) {
+    constexpr int kVals = 2 * NT * 4 * 32;  // fp32 sums of a tile
+    extern __shared__ __align__(128) float s_dyn[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float(*s_sum)[kW4Warps][kVals] = reinterpret_cast<float(*)[kW4Warps][kVals]>(s_dyn);
     const int r = lane >> 2, c = lane & 3;
     const int nkb = args.K / kW4Block;
     const SchedPtrs sp = sched_ptrs(args.sched, args.nseg);
     if constexpr (!DOWN) ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int64_t total = static_cast<int64_t>(sp.prefix[args.nseg]) * args.tiles;
-    bool waited = !DOWN;
-    for (int64_t task = static_cast<int64_t>(blockIdx.x) * (kW4Threads / 32) + (threadIdx.x >> 5);
-         task < total; task += static_cast<int64_t>(gridDim.x) * (kW4Threads / 32)) {
-        // segment: the last one whose first task is not behind this one
-        int lo = 0, hi = args.nseg - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (static_cast<int64_t>(sp.prefix[mid]) * args.tiles <= task) lo = mid;
-            else hi = mid - 1;
-        }
-        const int seg = lo;
-        const int chunks = sp.prefix[seg + 1] - sp.prefix[seg];
-        const int in_seg = static_cast<int>(task - static_cast<int64_t>(sp.prefix[seg]) * args.tiles);
-        const int tile = in_seg / chunks;
-        const int row0 = (in_seg - tile * chunks) * (8 * NT);
-        const int nrows = min(8 * NT, sp.rows[seg] - row0);
-        const bool special = seg == args.special;
-        const uint8_t* q = (special ? args.q_shared : args.q + seg * args.q_stride) +
-                           static_cast<int64_t>(tile) * nkb * kW4BlockBytes + lane * 32;
-        const __nv_bfloat16* sc = (special ? args.sc_shared : args.sc + seg * args.sc_stride) +
-                                  (static_cast<int64_t>(tile) * nkb * 8 + r) * SUB * 4;
-        W4Stage<SUB> st[2];
-        w4_load<SUB>(st[0], q, sc);
-        if (nkb > 1) w4_load<SUB>(st[1], q + kW4BlockBytes, sc + 32 * SUB);
-        if (!waited) {
-            ptx::grid_dep_wait();
-            waited = true;
-        }
-        // token rows: columns past the chunk's last row repeat it (not stored)
-        const __nv_bfloat16* b[NT];
+    const int ks = w4_ksplit(total / gridDim.x, nkb), per_cta = kW4Warps / ks;
+    const int slot = warp / ks, part = warp % ks;
+    const int kb0 = part * nkb / ks, kb1 = (part + 1) * nkb / ks;
+    // this CTA's run of tasks; a slot (KS warps) takes every per_cta-th
+    const int64_t begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+    const int rounds = static_cast<int>((end - begin + per_cta - 1) / per_cta);
+    const int tasks = begin + slot < end
+                          ? static_cast<int>((end - begin - slot + per_cta - 1) / per_cta)
+                          : 0;
+
+    W4Place at{};
+    const uint8_t* q = nullptr;
+    const uint8_t* sc = nullptr;
+    W4Stage<SUB> st[2];
+    auto load = [&](W4Stage<SUB>& s, int kb) {
+        if (kb < kb1) {
+            const uint8_t* p = q + static_cast<int64_t>(kb) * kW4BlockBytes;
+            ldg_stream(p, s.a[0]);
+            ldg_stream(p + 1024, s.a[1]);
+            p = sc + static_cast<int64_t>(kb) * 64 * SUB;
+            if constexpr (SUB == 1) {
+                s.s[0] = __ldg(reinterpret_cast<const uint2*>(p));
+            } else {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int row = sp.b_row0[seg] + row0 + min(8 * n + r, nrows - 1);
-            const int64_t at = (!DOWN && !special) ? args.row_src[row] : row;
-            b[n] = args.rows + at * args.K * (DOWN ? 2 : 1) + c * (DOWN ? 16 : 8);
+                for (int u = 0; u < SUB; u += 2) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + u * 8));
+                    s.s[u] = make_uint2(v.x, v.y);
+                    s.s[u + 1] = make_uint2(v.z, v.w);
+                }
+            }
         }
+    };
+    auto first_blocks = [&]() {
+        const bool special = at.seg == args.special;
+        const int64_t unit = static_cast<int64_t>(at.tile) * nkb;
+        q = (special ? args.q_shared : args.q + at.seg * args.q_stride) + unit * kW4BlockBytes +
+            lane * 32;
+        sc = reinterpret_cast<const uint8_t*>(
+            (special ? args.sc_shared : args.sc + at.seg * args.sc_stride) +
+            (unit * 8 + r) * SUB * 4);
+        load(st[0], kb0);
+        load(st[1], kb0 + 1);
+    };
+    if (tasks) {
+        at = w4_place(sp, args.nseg, args.tiles, begin + slot);
+        first_blocks();
+    }
+    if constexpr (DOWN) ptx::grid_dep_wait();  // (the weights and the schedule are older)
+
+    for (int round = 0; round < rounds; ++round) {
+        const bool mine = round < tasks;
+        const int row0 = at.chunk * (8 * NT);
+        int nrows = 0;
         float tot[2][NT][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -156,112 +289,179 @@ __global__ void __launch_bounds__(kW4Threads) w4_product_kernel(const W4Args arg
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tot[h][n][i] = 0.0f;
-
-        auto block = [&](const W4Stage<SUB>& s, int kb) {
-            float acc[2][NT][4];
+        if (mine) {
+            nrows = min(8 * NT, sp.rows[at.seg] - row0);
+            // token rows: lanes past the chunk's last row repeat it (not stored)
+            const uint8_t* b[NT];
 #pragma unroll
-            for (int k32 = 0; k32 < 4; ++k32) {
-                if (k32 % (4 / SUB) == 0) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[h][n][i] = 0.0f;
-                }
-                uint4 bv[NT], bl[DOWN ? NT : 1];
+            for (int n = 0; n < NT; ++n) {
+                int row = sp.b_row0[at.seg] + row0 + min(8 * n + r, nrows - 1);
+                if (!DOWN && at.seg != args.special) row = args.row_src[row];
+                b[n] = args.rows + (static_cast<int64_t>(row) * nkb + kb0) * kW4RowBlock + c * 16;
+            }
+            auto block = [&](const W4Stage<SUB>& s) {
+                // limb sums and scale of the lane's row r, then of columns 2c, 2c + 1
+                uint32_t sum[NT][2][SUB];
+                float scale[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const int64_t at = (static_cast<int64_t>(kb) * 128 + k32 * 32) * (DOWN ? 2 : 1);
-                    bv[n] = *reinterpret_cast<const uint4*>(b[n] + at);
-                    if constexpr (DOWN) bl[n] = *reinterpret_cast<const uint4*>(b[n] + at + 8);
-                }
+                    const uint32_t* m =
+                        reinterpret_cast<const uint32_t*>(b[n] + 2 * kW4Block - c * 16);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t f[4];
-                    w4_fragment(s.a[h][2 * k32], f);
+                    for (int u = 0; u <= SUB; ++u) {
+                        const uint32_t v = m[u];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma_bf16(acc[h][n], f, bv[n].x, bv[n].y);
-                        if constexpr (DOWN) mma_bf16(acc[h][n], f, bl[n].x, bl[n].y);
-                    }
-                    w4_fragment(s.a[h][2 * k32 + 1], f);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma_bf16(acc[h][n], f, bv[n].z, bv[n].w);
-                        if constexpr (DOWN) mma_bf16(acc[h][n], f, bl[n].z, bl[n].w);
-                    }
-                }
-                if ((k32 + 1) % (4 / SUB) == 0) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float2 sv = __bfloat1622float2(s.s[k32 / (4 / SUB)][h]);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            tot[h][n][0] = fmaf(sv.x, acc[h][n][0], tot[h][n][0]);
-                            tot[h][n][1] = fmaf(sv.x, acc[h][n][1], tot[h][n][1]);
-                            tot[h][n][2] = fmaf(sv.y, acc[h][n][2], tot[h][n][2]);
-                            tot[h][n][3] = fmaf(sv.y, acc[h][n][3], tot[h][n][3]);
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t o = __shfl_sync(0xffffffffu, v, 8 * c + 4 * j);
+                            if (u < SUB) sum[n][j][u] = o;
+                            else scale[n][j] = __uint_as_float(o);
                         }
                     }
                 }
-            }
-        };
-        for (int kb = 0; kb < nkb; kb += 2) {
-            block(st[0], kb);
-            if (kb + 2 < nkb) w4_load<SUB>(st[0], q + static_cast<int64_t>(kb + 2) * kW4BlockBytes, sc + static_cast<int64_t>(kb + 2) * 32 * SUB);
-            if (kb + 1 < nkb) {
-                block(st[1], kb + 1);
-                if (kb + 3 < nkb) w4_load<SUB>(st[1], q + static_cast<int64_t>(kb + 3) * kW4BlockBytes, sc + static_cast<int64_t>(kb + 3) * 32 * SUB);
-            }
-        }
-        // lane 4r + c holds rows r and r + 8 of both halves, columns 2c, 2c + 1
+                int32_t acc[2][2][NT][4];  // [limb hi, lo][half]
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+                for (int k64 = 0; k64 < 2; ++k64) {
+                    uint4 bv[NT][2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int col = 8 * n + 2 * c + j;
-                if (col >= nrows) continue;
-                const int64_t m = sp.out_row0[seg] + row0 + col;
-                if constexpr (!DOWN) {
-                    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(args.out) + m * args.ld * 2 +
-                                       tile * 32 + r;
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        float g = tot[0][n][2 * t + j], u = tot[1][n][2 * t + j];
-                        // compare-select clamp: NaN passes through
-                        g = g > args.clip ? args.clip : (g < -args.clip ? -args.clip : g);
-                        u = u > args.clip ? args.clip : (u < -args.clip ? -args.clip : u);
-                        const float v = g / (1.0f + __expf(-g)) * u;
-                        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                        // the remainder of a non-finite value would be NaN
-                        const float rem = v - __bfloat162float(hi);
-                        o[t * 16] = hi;
-                        o[t * 16 + 8] = __float2bfloat16_rn(isfinite(rem) ? rem : 0.0f);
+                        for (int l = 0; l < 2; ++l)
+                            bv[n][l] =
+                                *reinterpret_cast<const uint4*>(b[n] + k64 * 128 + l * 64);
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+                        const int k32 = 2 * k64 + kk;
+                        if (k32 % (4 / SUB) == 0) {
+                            // a group starts from -8 times the limb sum (row r + 8:
+                            // 16 u, hence -128 times)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const uint32_t v = sum[n][j][k32 / (4 / SUB)];
+                                    const int32_t hi = static_cast<int32_t>(v) >> 16;
+                                    const int32_t lo = static_cast<int16_t>(v & 0xffffu);
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h) {
+                                        acc[0][h][n][j] = kW4MagicBits - 8 * hi;
+                                        acc[0][h][n][2 + j] = kW4MagicBits - 128 * hi;
+                                        acc[1][h][n][j] = kW4MagicBits - 8 * lo;
+                                        acc[1][h][n][2 + j] = kW4MagicBits - 128 * lo;
+                                    }
+                                }
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t w0 = s.a[h][2 * k32], w1 = s.a[h][2 * k32 + 1];
+                            const uint32_t f[4] = {w0 & 0x0f0f0f0fu, w0 & 0xf0f0f0f0u,
+                                                   w1 & 0x0f0f0f0fu, w1 & 0xf0f0f0f0u};
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int l = 0; l < 2; ++l)
+                                    mma_u8s8(acc[l][h][n], f, kk ? bv[n][l].z : bv[n][l].x,
+                                             kk ? bv[n][l].w : bv[n][l].y);
+                        }
+                        if ((k32 + 1) % (4 / SUB) == 0) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint2 s2 = s.s[k32 / (4 / SUB)];
+                                const uint32_t sw = h ? s2.y : s2.x;
+                                const float2 sv = __bfloat1622float2(
+                                    *reinterpret_cast<const __nv_bfloat162*>(&sw));
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const float hi = __int_as_float(acc[0][h][n][i]) - kW4Magic;
+                                        const float lo = __int_as_float(acc[1][h][n][i]) - kW4Magic;
+                                        tot[h][n][i] = fmaf((i < 2 ? sv.x : sv.y) * scale[n][i & 1],
+                                                            fmaf(256.0f, hi, lo), tot[h][n][i]);
+                                    }
+                            }
+                        }
                     }
-                } else {
-                    const float wt = m < args.routed_rows ? args.row_w[m] : 1.0f;
-                    float* o = static_cast<float*>(args.out) + m * args.ld + tile * 32 + r;
+                }
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-                            o[h * 16 + t * 8] = wt * tot[h][n][2 * t + j];
+                for (int n = 0; n < NT; ++n) b[n] += kW4RowBlock;
+            };
+#pragma unroll 1
+            for (int kb = kb0; kb < kb1; kb += 2) {
+                block(st[0]);
+                load(st[0], kb + 2);
+                if (kb + 1 < kb1) {
+                    block(st[1]);
+                    load(st[1], kb + 3);
                 }
             }
         }
+        float* sums = s_sum[round & 1][warp];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sums[((h * NT + n) * 4 + i) * 32 + lane] = tot[h][n][i];
+        // the next tile's first blocks are on their way before this one is added up
+        const W4Place cur = at;
+        if (round + 1 < tasks) {
+            for (int i = 0; i < per_cta; ++i) w4_advance(at, sp, args.nseg, args.tiles);
+            first_blocks();
+        }
+        // (two buffers in turn: the barrier of the next round lies between this
+        // round's reads and the writes of the round after)
+        __syncthreads();
+        if (!mine) continue;
+        // lane 4r + c, value i: row r + 8 (i / 2) of half h, column 8n + 2c + i % 2
+        const float(*from)[kVals] = &s_sum[round & 1][slot * ks];
+        constexpr int kOut = DOWN ? kVals : kVals / 2;
+        for (int v = part * 32 + lane; v < kOut; v += ks * 32) {
+            const int i = (v >> 5) & 3, n = (v >> 7) % NT, h = v / (kVals / 2);
+            const int col = 8 * n + 2 * c + (i & 1);
+            if (col >= nrows) continue;
+            float g = 0.0f, u = 0.0f;
+            for (int w = 0; w < ks; ++w) {
+                g += from[w][v];
+                if constexpr (!DOWN) u += from[w][v + kVals / 2];
+            }
+            const int64_t row = sp.out_row0[cur.seg] + row0 + col;
+            if constexpr (!DOWN) {
+                if (i >= 2) {  // row r + 8 carries 16 u
+                    g *= 0.0625f;
+                    u *= 0.0625f;
+                }
+                // compare-select clamp: NaN passes through
+                g = g > args.clip ? args.clip : (g < -args.clip ? -args.clip : g);
+                u = u > args.clip ? args.clip : (u < -args.clip ? -args.clip : u);
+                args.out[row * args.ld + cur.tile * 16 + (i >> 1) * 8 + r] =
+                    g / (1.0f + __expf(-g)) * u;
+            } else {
+                const float wt = row < args.routed_rows ? args.row_w[row] : 1.0f;
+                args.out[row * args.ld + cur.tile * 32 + h * 16 + (i >> 1) * 8 + r] =
+                    wt * (i >= 2 ? 0.0625f * g : g);
+            }
+        }
     }
-    if (!waited) ptx::grid_dep_wait();
 }
 
-// Dispatch of up to kPermTokens tokens in one CTA of 512 threads: histogram,
-// offsets, tile schedules and stable positions (row order: expert, token), as
-// the three dispatch launches compute them for any number of tokens.  pos of
-// an assignment with an expert out of range is -1.
+// Dispatch of up to kPermTokens tokens in one CTA (the first) of 512 threads:
+// histogram, offsets, tile schedules and stable positions (row order: expert,
+// token), as the three dispatch launches compute them for any number of tokens.
+// pos of an assignment with an expert out of range is -1.  The other CTAs split
+// the token rows into limbs meanwhile.
 __global__ void __launch_bounds__(512) w4_dispatch_kernel(
     const int32_t* __restrict__ idx, const float* __restrict__ topk_w, int T, int E, int k,
     int num_shared, int nmax, int32_t* sched_gu, int32_t* sched_dn, int32_t* __restrict__ pos,
-    int32_t* __restrict__ src, float* __restrict__ row_w, int32_t* status) {
+    int32_t* __restrict__ src, float* __restrict__ row_w, int32_t* status,
+    const __nv_bfloat16* __restrict__ x, int64_t units, int sub,
+    uint8_t* __restrict__ row_blocks) {
+    if (blockIdx.x > 0) {
+        ptx::grid_dep_wait();
+        ptx::grid_dep_launch();
+        const int64_t unit = (static_cast<int64_t>(blockIdx.x) - 1) * 16 + (threadIdx.x >> 5);
+        if (unit < units) w4_split_block<__nv_bfloat16>(x, sub, unit, row_blocks);
+        return;
+    }
     __shared__ uint32_t masks[kPermWarps][kMaxExperts];
     __shared__ int32_t wbase[kPermWarps][kMaxExperts];
     __shared__ int s_warp[32];

@@ -191,26 +191,34 @@ def w4_weights(q, sc, I, H, group):
 def w4_ffn(x, mats, clip, group):
     """FFN of rows x in fp64 and a bound on the kernel's error before the output rounding.
 
-    A tensor-core product of K terms is K/16 MMAs and K/group fp32 additions, each
-    off by at most 2^-22 of the magnitudes added so far (the MMA adds 16 products
-    and the accumulator with truncation); the clamp only shrinks errors;
-    |silu'| <= 1.1; exp, sum and quotient: 2^-20 of h; h as bf16 high + low parts
-    keeps 2^-16 of itself."""
+    The kernel takes a row's block of 128 values as 16-bit integers times a power
+    of two a; the largest, amax, is 16191 a or more, so each value is off by at
+    most a/2 <= 2^-14.9 amax.  Its sums over a group are exact integers; the
+    two limbs are joined, scaled (two products) and added to the fp32 total, in
+    K/group additions and 8 more over the warps: each of these steps is off by at
+    most 2^-24 of the magnitudes added so far.  The clamp only shrinks errors;
+    |silu'| <= 1.1; exp, sum and quotient: 2^-20 of h."""
     gate, up, down = mats
     H, I = gate.shape[1], gate.shape[0]
-    unit = 2.0 ** -22
-    eg = (H / 16 + H / group + 2) * unit
+
+    def floor(v):  # 2^-14.9 of each block's largest magnitude
+        return (v.abs().reshape(v.shape[0], -1, 128).amax(-1) * 2.0 ** -14.9
+                ).repeat_interleave(128, -1)
+
+    def product(v, dv, m):
+        e = (m.shape[1] / group + 8 + 3) * 2.0 ** -24
+        return v @ m.T, dv @ m.abs().T + e * ((v.abs() + dv) @ m.abs().T)
+
     x = x.to(F64)
-    g, u = x @ gate.T, x @ up.T
-    dg, du = eg * (x.abs() @ gate.abs().T), eg * (x.abs() @ up.abs().T)
+    g, dg = product(x, floor(x), gate)
+    u, du = product(x, floor(x), up)
     if clip > 0:
         g, u = g.clamp(-clip, clip), u.clamp(-clip, clip)
     silu = g * torch.sigmoid(g)
     h = silu * u
-    dh = 1.1 * dg * (u.abs() + du) + silu.abs() * du + (2.0 ** -20 + 2.0 ** -16) * h.abs()
-    ed = (I / 8 + I / group + 2) * unit
-    mag = (h.abs() + dh) @ down.abs().T
-    return h @ down.T, dh @ down.abs().T + ed * mag
+    dh = 1.1 * dg * (u.abs() + du) + silu.abs() * du + 2.0 ** -20 * h.abs()
+    dh = dh + 2.0 ** -24 * (h.abs() + dh) + floor(h.abs() + dh)
+    return product(h, dh, down)
 
 
 def w4_layer(x, idx, w, experts, shared, clip, group):
