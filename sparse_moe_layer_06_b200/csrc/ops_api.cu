@@ -115,12 +115,14 @@ int32_t check_w4(const moe_problem* p, int32_t group) {
     MOE_TRY(check_problem(p));
     if (p->H % kW4Block != 0 || p->I % kW4Block != 0) return MOE_ERR_UNSUPPORTED;
     if (group != 32 && group != 64 && group != 128) return MOE_ERR_UNSUPPORTED;
+    // a chunk of one row has to fit in a CTA's shared memory
+    if (p->H > kW4MaxK || p->I > kW4MaxK) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
 struct W4Layout {
     size_t status, route, idx, w, hist, base, counts, offsets, sched_gu, sched_dn, pos, src,
-        row_w, x_rows, h, h_rows, y, total;
+        row_w, x_rows, x_meta, h, h_rows, h_meta, y, total;
 };
 
 W4Layout w4_layout(const moe_problem* p, bool with_route) {
@@ -142,42 +144,43 @@ W4Layout w4_layout(const moe_problem* p, bool with_route) {
     L.pos = c.take(T * k * 4);
     L.src = c.take(T * k * 4);
     L.row_w = c.take(T * k * 4);
-    L.x_rows = c.take(T * (H / kW4Block) * kW4RowBlock);
+    L.x_rows = c.take(T * H * 2);
+    L.x_meta = c.take(T * (H / kW4Block) * kW4MaxMeta * 4);
     L.h = c.take(T * (k + S) * I * 4);
-    L.h_rows = c.take(T * (k + S) * (I / kW4Block) * kW4RowBlock);
+    L.h_rows = c.take(T * (k + S) * I * 2);
+    L.h_meta = c.take(T * (k + S) * (I / kW4Block) * kW4MaxMeta * 4);
     L.y = c.take(T * (k + S) * H * 4);
     L.total = c.off;
     return L;
 }
 
 // 8-row column tiles per task, from the mean rows per expert.
-int w4_column_tiles(double mean_rows) {
-    if (mean_rows <= 3.0) return 1;
-    if (mean_rows <= 10.0) return 2;
-    return 4;
+int w4_column_tiles(double mean_rows) { return mean_rows <= 3.0 ? 1 : 2; }
+
+int w4_cap(int nt, int64_t K, int sub) {
+    return nt == 1 ? w4_rows_cap<1>(K, sub) : w4_rows_cap<2>(K, sub);
 }
 
 template <int NT, bool DOWN, int SUB>
 int32_t launch_w4_n(const W4Args& a, int64_t max_tasks, cudaStream_t s) {
     auto kern = w4_product_kernel<NT, DOWN, SUB>;
+    constexpr int threads = W4Shape<NT>::kWarps * 32;
     int dev = 0;
     cudaGetDevice(&dev);
-    static std::atomic<int> per_sm[64];
-    int n = dev < 64 ? per_sm[dev].load() : 0;
-    constexpr int smem = 2 * kW4Warps * 2 * NT * 128 * 4;  // two buffers of partial sums
-    if (n == 0) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-                cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kW4Threads, smem) !=
-                cudaSuccess ||
-            n < 1)
+    static std::atomic<uint64_t> configured{0};
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!bit || !(configured.load() & bit)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
+            cudaSuccess)
             return MOE_ERR_CUDA;
-        if (dev < 64) per_sm[dev].store(n);
+        configured.fetch_or(bit);
     }
-    const int grid = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>(static_cast<int64_t>(sm_count()) * n, max_tasks)));
+    const int smem = W4Shape<NT>::kSumBytes +
+                     a.K / kW4Block * a.cap * (kW4RowBytes + 4 * w4_meta_words(SUB));
+    const int grid =
+        static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sm_count(), max_tasks)));
     MOE_LAUNCH(DOWN ? "expert_down_w4" : "expert_gate_up_w4", s,
-               if (launch_ex(kern, grid, kW4Threads, smem, s, pdl_enabled(), a) != cudaSuccess)
+               if (launch_ex(kern, grid, threads, smem, s, pdl_enabled(), a) != cudaSuccess)
                    return MOE_ERR_CUDA);
     return MOE_OK;
 }
@@ -192,9 +195,6 @@ int32_t launch_w4(int nt, int group, const W4Args& a, int64_t max_tasks, cudaStr
         case 2032: return launch_w4_n<2, DOWN, 4>(a, max_tasks, s);
         case 2064: return launch_w4_n<2, DOWN, 2>(a, max_tasks, s);
         case 2128: return launch_w4_n<2, DOWN, 1>(a, max_tasks, s);
-        case 4032: return launch_w4_n<4, DOWN, 4>(a, max_tasks, s);
-        case 4064: return launch_w4_n<4, DOWN, 2>(a, max_tasks, s);
-        case 4128: return launch_w4_n<4, DOWN, 1>(a, max_tasks, s);
         default: return MOE_ERR_UNSUPPORTED;
     }
 }
@@ -209,35 +209,38 @@ int32_t run_experts_w4(const moe_problem* p, int32_t group, const void* x, const
     int32_t* pos = at<int32_t>(ws, L.pos);
     int32_t* src = at<int32_t>(ws, L.src);
     float* row_w = at<float>(ws, L.row_w);
-    const int nt = w4_column_tiles(static_cast<double>(T * k) / E);
-    const bool pdl = pdl_enabled();
     const int sub = kW4Block / group;
+    const int nt = w4_column_tiles(static_cast<double>(T * k) / E);
+    const int cap_gu = w4_cap(nt, H, sub), cap_dn = w4_cap(nt, I, sub);
+    const bool pdl = pdl_enabled();
     const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
     uint8_t* x_rows = at<uint8_t>(ws, L.x_rows);
+    uint32_t* x_meta = at<uint32_t>(ws, L.x_meta);
     const int64_t x_units = T * (H / kW4Block);
     if (T <= kPermTokens) {
         MOE_LAUNCH("dispatch_w4", s,
                    if (launch_ex(w4_dispatch_kernel, 1 + static_cast<int>((x_units + 15) / 16),
                                  512, 0, s, pdl, idx, w, static_cast<int>(T), p->E, p->top_k,
-                                 p->num_shared, 8 * nt, sg, sd, pos, src, row_w, status, xb,
-                                 x_units, sub, x_rows) != cudaSuccess)
+                                 p->num_shared, sg, cap_gu, sd, cap_dn, pos, src, row_w, status,
+                                 xb, x_units, sub, x_rows, x_meta) != cudaSuccess)
                        return MOE_ERR_CUDA);
     } else {
         // (an assignment with an expert out of range keeps position -1)
         if (cudaMemsetAsync(pos, 0xff, static_cast<size_t>(T * k) * 4, s) != cudaSuccess)
             return MOE_ERR_CUDA;
         MOE_TRY(dispatch_rows(p, idx, w, at<int32_t>(ws, L.hist), at<int32_t>(ws, L.base),
-                              at<int32_t>(ws, L.counts), at<int32_t>(ws, L.offsets), sg, 8 * nt,
-                              sd, 8 * nt, pos, src, row_w, status, s));
+                              at<int32_t>(ws, L.counts), at<int32_t>(ws, L.offsets), sg, cap_gu,
+                              sd, cap_dn, pos, src, row_w, status, s));
         MOE_LAUNCH("split_rows_w4", s,
                    if (launch_ex(w4_split_kernel<__nv_bfloat16>,
                                  static_cast<int>((x_units + 7) / 8), 256, 0, s, pdl, xb, x_units,
-                                 sub, x_rows) != cudaSuccess) return MOE_ERR_CUDA);
+                                 sub, x_rows, x_meta) != cudaSuccess) return MOE_ERR_CUDA);
     }
     const int nseg = static_cast<int>(E + S);
-    // at most this many chunks of 8 nt rows over all segments
-    const int64_t chunks = std::min<int64_t>(T * k, T * k / (8 * nt) + E) +
-                           (S ? (T + 8 * nt - 1) / (8 * nt) : 0);
+    // at most this many chunks of `cap` rows over all segments
+    const auto max_chunks = [&](int64_t cap) {
+        return std::min<int64_t>(T * k, T * k / cap + E) + (S ? (T + cap - 1) / cap : 0);
+    };
     W4Args a{};
     a.nseg = nseg;
     a.special = S ? static_cast<int32_t>(E) : -1;
@@ -253,16 +256,19 @@ int32_t run_experts_w4(const moe_problem* p, int32_t group, const void* x, const
     a.sc_shared = static_cast<const __nv_bfloat16*>(ss);
     a.sched = sg;
     a.rows = x_rows;
+    a.meta = x_meta;
+    a.cap = cap_gu;
     a.K = static_cast<int32_t>(H);
     a.tiles = static_cast<int32_t>(I / 16);
     a.out = at<float>(ws, L.h);
     a.ld = static_cast<int32_t>(I);
-    MOE_TRY(launch_w4<false>(nt, group, a, chunks * a.tiles, s));
+    MOE_TRY(launch_w4<false>(nt, group, a, max_chunks(cap_gu) * a.tiles, s));
     const int64_t h_units = T * (k + S) * (I / kW4Block);
     uint8_t* h_rows = at<uint8_t>(ws, L.h_rows);
+    uint32_t* h_meta = at<uint32_t>(ws, L.h_meta);
     MOE_LAUNCH("split_h_w4", s,
                if (launch_ex(w4_split_kernel<float>, static_cast<int>((h_units + 7) / 8), 256, 0,
-                             s, pdl, static_cast<const float*>(a.out), h_units, sub, h_rows) !=
+                             s, pdl, static_cast<const float*>(a.out), h_units, sub, h_rows, h_meta) !=
                    cudaSuccess) return MOE_ERR_CUDA);
     a.q = eq + I * H;
     a.sc = static_cast<const __nv_bfloat16*>(es) + 2 * I * H / group;
@@ -270,11 +276,13 @@ int32_t run_experts_w4(const moe_problem* p, int32_t group, const void* x, const
     a.sc_shared = ss ? static_cast<const __nv_bfloat16*>(ss) + 2 * I * H / group : nullptr;
     a.sched = sd;
     a.rows = h_rows;
+    a.meta = h_meta;
+    a.cap = cap_dn;
     a.K = static_cast<int32_t>(I);
     a.tiles = static_cast<int32_t>(H / 32);
     a.out = at<float>(ws, L.y);
     a.ld = static_cast<int32_t>(H);
-    MOE_TRY(launch_w4<true>(nt, group, a, chunks * a.tiles, s));
+    MOE_TRY(launch_w4<true>(nt, group, a, max_chunks(cap_dn) * a.tiles, s));
     return combine_rows_f32(p, at<float>(ws, L.y), pos, static_cast<__nv_bfloat16*>(out), status,
                             s);
 }

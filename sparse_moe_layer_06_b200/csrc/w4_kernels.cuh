@@ -27,9 +27,9 @@
 // word 2a + b of its 8 the k = 32 a + 8 c + 4 b + {0, 2, 1, 3} (one per byte):
 // with both words of a, the A fragments of one MMA.
 // Scales: [tile][block][r 8][128/G][half][r, r + 8] bf16.
-// Limbs of a row and block: [a / 2][limb][c 4][a % 2][8 bytes], the 8 bytes in
-// the order of the two words; behind them the limb sums of each group (two
-// int16) and the scale, in 32 bytes.
+// Limbs of a row and block, 256 bytes: [a / 2][limb][c 4][a % 2][8 bytes], the 8
+// bytes in the order of the two words; in an array of their own the limb sums of
+// each group (two int16) and the scale, W4Meta words per row and block.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -42,8 +42,31 @@ namespace moe {
 
 constexpr int kW4Block = 128;       // contraction length of a block
 constexpr int kW4BlockBytes = 2048; // codes of a pair tile's block
-constexpr int kW4Threads = 256;
-constexpr int kW4Warps = kW4Threads / 32;
+constexpr int kW4RowBytes = 256;    // limbs of a row's block
+constexpr int kW4MaxK = 65536;      // longest contraction (a row's limbs: 147 KB)
+
+// Shape of a launch whose tasks have up to 8 NT rows: warps of a CTA (one CTA
+// per SM) and weight blocks that each warp has on the way in registers.  One
+// column tile leaves 128 registers a thread and so 16 warps; two take more.
+template <int NT>
+struct W4Shape {
+    static constexpr int kWarps = NT == 1 ? 16 : 8;
+    static constexpr int kStages = NT == 1 ? 2 : 3;
+    static constexpr int kVals = 2 * NT * 4 * 32;             // fp32 sums of a tile
+    static constexpr int kSumBytes = 2 * kWarps * kVals * 4;  // two buffers of them
+};
+
+// Words per row and block of the group sums and the scale, for SUB groups.
+__host__ __device__ constexpr int w4_meta_words(int sub) { return sub == 1 ? 2 : (sub == 2 ? 4 : 8); }
+constexpr int kW4MaxMeta = 8;
+
+// Rows of K values that fit beside the sums in a CTA's shared memory, at most 8 NT.
+template <int NT>
+int w4_rows_cap(int64_t K, int sub) {
+    const int64_t row = K / kW4Block * (kW4RowBytes + 4 * w4_meta_words(sub));
+    const int64_t cap = (227 * 1024 - W4Shape<NT>::kSumBytes) / row;
+    return static_cast<int>(cap < 8 * NT ? cap : 8 * NT);
+}
 
 struct W4Args {
     const uint8_t* q;          // codes of expert 0's matrix
@@ -51,11 +74,12 @@ struct W4Args {
     const uint8_t* q_shared;   // the same of the shared expert (segment `special`)
     const __nv_bfloat16* sc_shared;
     int64_t q_stride, sc_stride;  // bytes / scales from one expert to the next
-    const int32_t* sched;      // tile schedule of nseg segments (chunk j: rows from j * 8 NT)
+    const int32_t* sched;      // tile schedule of nseg segments (chunk j: rows from j * cap)
     int32_t nseg, special;
-    const uint8_t* rows;       // row blocks of the token rows
+    const uint8_t* rows;       // limbs of the token rows
+    const uint32_t* meta;      // their group sums and scales
     const int32_t* row_src;    // gate/up: token of each routed row (special: the row itself)
-    int32_t K, tiles;          // contraction length, pair tiles
+    int32_t K, tiles, cap;     // contraction length, pair tiles, rows of a chunk
     float* out;                // gate/up: h rows, down: weighted rows; fp32 [*, ld]
     int32_t ld;
     const float* row_w;        // down: routing weight of each routed row
@@ -74,9 +98,6 @@ __device__ __forceinline__ void mma_u8s8(int32_t (&d)[4], const uint32_t (&a)[4]
 
 constexpr int32_t kW4MagicBits = 0x4b400000;   // 1.5 * 2^23 as fp32
 constexpr float kW4Magic = 12582912.0f;
-
-// Bytes of a row's block: two limbs of 128 values, the group sums, the scale.
-constexpr int kW4RowBlock = 2 * kW4Block + 32;
 
 // 32 bytes that are read once: past L1, first to leave L2.
 __device__ __forceinline__ void ldg_stream(const void* p, uint32_t (&v)[8]) {
@@ -101,7 +122,8 @@ struct W4Stage {
 // are NaN.
 template <typename T>
 __device__ __forceinline__ void w4_split_block(const T* __restrict__ rows, int sub, int64_t unit,
-                                               uint8_t* __restrict__ out) {
+                                               uint8_t* __restrict__ out,
+                                               uint32_t* __restrict__ meta) {
     const int lane = threadIdx.x & 31;
     float v[4];
     const T* in = rows + unit * kW4Block + lane * 4;
@@ -131,9 +153,8 @@ __device__ __forceinline__ void w4_split_block(const T* __restrict__ rows, int s
     n = min(max(n, -126), 126);
     const float scale = __uint_as_float(static_cast<uint32_t>(n + 127) << 23);
     const float inv = __uint_as_float(static_cast<uint32_t>(127 - n) << 23);
-    out += unit * kW4RowBlock;
-    uint32_t* meta = reinterpret_cast<uint32_t*>(out + 2 * kW4Block);
-    out += (lane >> 4) * 128 + ((lane & 7) >> 1) * 16 + ((lane >> 3) & 1) * 8 + (lane & 1) * 4;
+    meta += unit * w4_meta_words(sub);
+    out += unit * kW4RowBytes + (lane >> 4) * 128 + ((lane & 7) >> 1) * 16 + ((lane >> 3) & 1) * 8 + (lane & 1) * 4;
     uint32_t hi = 0, lo = 0;
     int sum_hi = 0, sum_lo = 0;
 #pragma unroll
@@ -161,88 +182,116 @@ __device__ __forceinline__ void w4_split_block(const T* __restrict__ rows, int s
 
 template <typename T>
 __global__ void __launch_bounds__(256) w4_split_kernel(const T* __restrict__ rows, int64_t units,
-                                                       int sub, uint8_t* __restrict__ out) {
+                                                       int sub, uint8_t* __restrict__ out,
+                                                       uint32_t* __restrict__ meta) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (unit < units) w4_split_block<T>(rows, sub, unit, out);
+    if (unit < units) w4_split_block<T>(rows, sub, unit, out, meta);
 }
 
-// Where a CTA's next tile lies: its segment and chunk of token rows.
-struct W4Place {
-    int seg, tile, chunk, chunks;
+// A round of a CTA: `tiles` tiles from `tile` on of one chunk of rows, each
+// shared by 2^log_ks warps.
+struct W4Round {
+    int seg, chunk;   // segment, and chunk within it
+    int tile, tiles;
+    int log_ks;
+    int left;         // tasks of the CTA behind this round
 };
 
-// Task t of the launch, tasks numbered (segment, tile, chunk): the segment is
-// the last one whose first task is not behind t.
-__device__ __forceinline__ W4Place w4_place(const SchedPtrs& sp, int nseg, int tiles, int64_t t) {
+// Segment of chunk g of the launch: the last whose first chunk is not behind it.
+__device__ __forceinline__ int w4_segment(const SchedPtrs& sp, int nseg, int g) {
     int lo = 0, hi = nseg - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (static_cast<int64_t>(sp.prefix[mid]) * tiles <= t) lo = mid;
+        if (sp.prefix[mid] <= g) lo = mid;
         else hi = mid - 1;
     }
-    W4Place p;
-    p.seg = lo;
-    p.chunks = sp.prefix[lo + 1] - sp.prefix[lo];
-    const int in_seg = static_cast<int>(t - static_cast<int64_t>(sp.prefix[lo]) * tiles);
-    p.tile = in_seg / p.chunks;
-    p.chunk = in_seg - p.tile * p.chunks;
-    return p;
+    return lo;
 }
 
-// The task behind p (if there is one: empty segments are passed over).
-__device__ __forceinline__ void w4_advance(W4Place& p, const SchedPtrs& sp, int nseg, int tiles) {
-    if (++p.chunk < p.chunks) return;
-    p.chunk = 0;
-    if (++p.tile < tiles) return;
-    p.tile = 0;
-    do {
-        ++p.seg;
-        p.chunks = p.seg < nseg ? sp.prefix[p.seg + 1] - sp.prefix[p.seg] : 1;
-    } while (p.chunks == 0);
+// The round behind `p` (p.tiles = 0: the first one, p.tile its tile): as many
+// tiles as the warps hold at 2^base warps each, or, for fewer tiles than that,
+// as many as keep all warps busy.
+template <int kWarps>
+__device__ __forceinline__ void w4_next_round(W4Round& p, const SchedPtrs& sp, int all_tiles,
+                                              int nseg, int base, int most) {
+    p.tile += p.tiles;
+    if (p.tile == all_tiles) {
+        p.tile = 0;
+        if (sp.prefix[p.seg] + ++p.chunk == sp.prefix[p.seg + 1]) {
+            p.chunk = 0;
+            do ++p.seg;
+            while (p.seg + 1 < nseg && sp.prefix[p.seg] == sp.prefix[p.seg + 1]);
+        }
+    }
+    const int rem = min(all_tiles - p.tile, p.left);
+    int l = base;
+    while (l < most && (kWarps >> l) > rem) ++l;
+    p.log_ks = l;
+    p.tiles = min(kWarps >> l, rem);
+    p.left -= p.tiles;
 }
 
-// Warps that share a tile, for CTAs with `run` tiles each: one where that many
-// rounds keep every warp busy, else all that the contraction has blocks for.
-__device__ __forceinline__ int w4_ksplit(int64_t run, int nkb) {
-    const int most = nkb >= 8 ? 8 : (nkb >= 4 ? 4 : (nkb >= 2 ? 2 : 1));
-    return run >= 96 ? min(2, most) : most;
-}
-
-// A CTA takes a run of consecutive tasks, each a pair tile against up to 8 NT
-// token rows of one segment.  Its warps split the contraction: KS of them share
-// a tile (8 / KS tiles at a time), warp k of them taking the k-th part of the
+// One CTA per SM takes a run of consecutive tasks, numbered (segment, chunk,
+// tile), each a pair tile against the chunk's rows.  The chunk's limbs lie in
+// shared memory (16-byte piece p of a row and block at p ^ 4 (row % 2), so that
+// the 8 lanes of a read meet different banks): taken through L1 instead, they
+// cost more than the weights, 700 against 456 us for the gate/up weights of 222
+// experts (2.9 GB).  2^log_ks warps share a tile, each with a part of its
 // blocks; their fp32 sums are added in shared memory in warp order.  The weights
-// stream through registers, two blocks ahead, past L1, which keeps the token
-// rows that the warps share.
+// stream through registers, kStages blocks ahead and across rounds, past L1.
 template <int NT, bool DOWN, int SUB>
-__global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
     w4_product_kernel(const W4Args args) {
-    constexpr int kVals = 2 * NT * 4 * 32;  // fp32 sums of a tile
-    extern __shared__ __align__(128) float s_dyn[];
+    using S = W4Shape<NT>;
+    constexpr int kWarps = S::kWarps, kStages = S::kStages, kVals = S::kVals;
+    constexpr int kMeta = w4_meta_words(SUB);
+    extern __shared__ __align__(128) uint8_t s_dyn[];
+    float(*s_sum)[kWarps][kVals] = reinterpret_cast<float(*)[kWarps][kVals]>(s_dyn);
+    uint8_t* s_rows = s_dyn + S::kSumBytes;  // [block][cap rows][256]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float(*s_sum)[kW4Warps][kVals] = reinterpret_cast<float(*)[kW4Warps][kVals]>(s_dyn);
     const int r = lane >> 2, c = lane & 3;
-    const int nkb = args.K / kW4Block;
+    const int nkb = args.K / kW4Block, cap = args.cap;
+    uint32_t* s_meta = reinterpret_cast<uint32_t*>(s_rows + nkb * cap * kW4RowBytes);
     const SchedPtrs sp = sched_ptrs(args.sched, args.nseg);
     if constexpr (!DOWN) ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    const int64_t total = static_cast<int64_t>(sp.prefix[args.nseg]) * args.tiles;
-    const int ks = w4_ksplit(total / gridDim.x, nkb), per_cta = kW4Warps / ks;
-    const int slot = warp / ks, part = warp % ks;
-    const int kb0 = part * nkb / ks, kb1 = (part + 1) * nkb / ks;
-    // this CTA's run of tasks; a slot (KS warps) takes every per_cta-th
-    const int64_t begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
-    const int rounds = static_cast<int>((end - begin + per_cta - 1) / per_cta);
-    const int tasks = begin + slot < end
-                          ? static_cast<int>((end - begin - slot + per_cta - 1) / per_cta)
-                          : 0;
+    // this CTA's run of tasks
+    const int groups = sp.prefix[args.nseg];
+    const int64_t total = static_cast<int64_t>(groups) * args.tiles;
+    const int64_t begin = total * blockIdx.x / gridDim.x;
+    const int run = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x - begin);
+    if (run == 0) {
+        if constexpr (DOWN) ptx::grid_dep_wait();
+        return;
+    }
+    // warps per tile: the fewest blocks on any warp's way, a round counting as
+    // two more for its barrier and sums
+    int most = 0, base = 0;
+    while ((2 << most) <= min(kWarps, nkb)) ++most;
+    for (int l = 0, best = 0x7fffffff; l <= most; ++l) {
+        const int cost = ((run + (kWarps >> l) - 1) / (kWarps >> l)) * (((nkb - 1) >> l) + 3);
+        if (cost < best) {
+            best = cost;
+            base = l;
+        }
+    }
 
-    W4Place at{};
+    W4Round cur{};
+    {
+        const int g = static_cast<int>(begin / args.tiles);
+        cur.seg = w4_segment(sp, args.nseg, g);
+        cur.chunk = g - sp.prefix[cur.seg];
+        cur.tile = static_cast<int>(begin - static_cast<int64_t>(g) * args.tiles);
+        cur.left = run;
+        w4_next_round<kWarps>(cur, sp, args.tiles, args.nseg, base, most);
+    }
+    // the warp's part of a round: tile slot, blocks [kb0, kb1)
+    int slot = 0, kb0 = 0, kb1 = 0;
     const uint8_t* q = nullptr;
     const uint8_t* sc = nullptr;
-    W4Stage<SUB> st[2];
+    W4Stage<SUB> st[kStages];
     auto load = [&](W4Stage<SUB>& s, int kb) {
         if (kb < kb1) {
             const uint8_t* p = q + static_cast<int64_t>(kb) * kW4BlockBytes;
@@ -261,27 +310,47 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1)
             }
         }
     };
-    auto first_blocks = [&]() {
-        const bool special = at.seg == args.special;
-        const int64_t unit = static_cast<int64_t>(at.tile) * nkb;
-        q = (special ? args.q_shared : args.q + at.seg * args.q_stride) + unit * kW4BlockBytes +
+    auto first_blocks = [&](const W4Round& p) {
+        const int part = warp & ((1 << p.log_ks) - 1);
+        slot = warp >> p.log_ks;
+        kb0 = part * nkb >> p.log_ks;
+        kb1 = slot < p.tiles ? (part + 1) * nkb >> p.log_ks : kb0;
+        const bool special = p.seg == args.special;
+        const int64_t unit = static_cast<int64_t>(p.tile + slot) * nkb;
+        q = (special ? args.q_shared : args.q + p.seg * args.q_stride) + unit * kW4BlockBytes +
             lane * 32;
         sc = reinterpret_cast<const uint8_t*>(
-            (special ? args.sc_shared : args.sc + at.seg * args.sc_stride) +
+            (special ? args.sc_shared : args.sc + p.seg * args.sc_stride) +
             (unit * 8 + r) * SUB * 4);
-        load(st[0], kb0);
-        load(st[1], kb0 + 1);
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) load(st[i], kb0 + i);
     };
-    if (tasks) {
-        at = w4_place(sp, args.nseg, args.tiles, begin + slot);
-        first_blocks();
-    }
+    // the chunk's rows into shared memory (asynchronous copies of this thread)
+    auto fetch_rows = [&](const W4Round& p) {
+        const int row0 = p.chunk * cap, nrows = min(cap, sp.rows[p.seg] - row0);
+        const int first = sp.b_row0[p.seg] + row0;
+        const bool direct = DOWN || p.seg == args.special;
+        for (int row = warp; row < nrows; row += kWarps) {
+            const int64_t m = (direct ? first + row : args.row_src[first + row]);
+            const uint8_t* src = args.rows + m * nkb * kW4RowBytes;
+            for (int i = lane; i < nkb * 16; i += 32)
+                ptx::cp_async_16(s_rows + ((i >> 4) * cap + row) * kW4RowBytes +
+                                     ((i & 15) ^ ((row & 1) * 4)) * 16,
+                                 src + i * 16, 16);
+            const uint32_t* meta = args.meta + m * nkb * kMeta;
+            for (int i = lane; i < nkb * kMeta; i += 32)
+                s_meta[((i / kMeta) * cap + row) * kMeta + i % kMeta] = meta[i];
+        }
+    };
+    first_blocks(cur);
     if constexpr (DOWN) ptx::grid_dep_wait();  // (the weights and the schedule are older)
+    fetch_rows(cur);
+    ptx::cp_async_wait_all();
+    __syncthreads();
 
-    for (int round = 0; round < rounds; ++round) {
-        const bool mine = round < tasks;
-        const int row0 = at.chunk * (8 * NT);
-        int nrows = 0;
+    for (int buffer = 0;; buffer ^= 1) {
+        const int row0 = cur.chunk * cap;
+        const int nrows = min(cap, sp.rows[cur.seg] - row0);
         float tot[2][NT][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -289,158 +358,176 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tot[h][n][i] = 0.0f;
-        if (mine) {
-            nrows = min(8 * NT, sp.rows[at.seg] - row0);
-            // token rows: lanes past the chunk's last row repeat it (not stored)
-            const uint8_t* b[NT];
+        // the lane's row of each 8 (those past the last repeat it, not stored),
+        // and its columns' sums and scales
+        uint32_t b[NT], m[NT][2];  // offsets into s_rows and s_meta
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                int row = sp.b_row0[at.seg] + row0 + min(8 * n + r, nrows - 1);
-                if (!DOWN && at.seg != args.special) row = args.row_src[row];
-                b[n] = args.rows + (static_cast<int64_t>(row) * nkb + kb0) * kW4RowBlock + c * 16;
-            }
-            auto block = [&](const W4Stage<SUB>& s) {
-                // limb sums and scale of the lane's row r, then of columns 2c, 2c + 1
-                uint32_t sum[NT][2][SUB];
-                float scale[NT][2];
+        for (int n = 0; n < NT; ++n) {
+            const int row = min(8 * n + r, nrows - 1);
+            b[n] = (kb0 * cap + row) * kW4RowBytes + (c ^ ((row & 1) * 4)) * 16;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint32_t* m =
-                        reinterpret_cast<const uint32_t*>(b[n] + 2 * kW4Block - c * 16);
+            for (int j = 0; j < 2; ++j)
+                m[n][j] = (kb0 * cap + min(8 * n + 2 * c + j, nrows - 1)) * kMeta;
+        }
+        auto block = [&](const W4Stage<SUB>& s) {
+            uint32_t sum[NT][2][SUB];
+            float scale[NT][2];
 #pragma unroll
-                    for (int u = 0; u <= SUB; ++u) {
-                        const uint32_t v = m[u];
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const uint32_t o = __shfl_sync(0xffffffffu, v, 8 * c + 4 * j);
-                            if (u < SUB) sum[n][j][u] = o;
-                            else scale[n][j] = __uint_as_float(o);
+                for (int j = 0; j < 2; ++j) {
+                    if constexpr (SUB == 1) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(s_meta + m[n][j]);
+                        sum[n][j][0] = v.x;
+                        scale[n][j] = __uint_as_float(v.y);
+                    } else {
+                        const uint4 v = *reinterpret_cast<const uint4*>(s_meta + m[n][j]);
+                        sum[n][j][0] = v.x;
+                        sum[n][j][1] = v.y;
+                        if constexpr (SUB == 4) {
+                            sum[n][j][2] = v.z;
+                            sum[n][j][3] = v.w;
                         }
+                        scale[n][j] = __uint_as_float(SUB == 2 ? v.z : s_meta[m[n][j] + 4]);
                     }
+                    m[n][j] += cap * kMeta;
                 }
-                int32_t acc[2][2][NT][4];  // [limb hi, lo][half]
+            int32_t acc[2][2][NT][4];  // [limb hi, lo][half]
 #pragma unroll
-                for (int k64 = 0; k64 < 2; ++k64) {
-                    uint4 bv[NT][2];
+            for (int k64 = 0; k64 < 2; ++k64) {
+                uint4 bv[NT][2];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int l = 0; l < 2; ++l)
-                            bv[n][l] =
-                                *reinterpret_cast<const uint4*>(b[n] + k64 * 128 + l * 64);
+                    for (int l = 0; l < 2; ++l)
+                        // (piece 8 k64 + 4 l + c, its bit 2 flipped in odd rows)
+                        bv[n][l] = *reinterpret_cast<const uint4*>(s_rows + (b[n] ^ (l * 64)) +
+                                                                   k64 * 128);
 #pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) {
-                        const int k32 = 2 * k64 + kk;
-                        if (k32 % (4 / SUB) == 0) {
-                            // a group starts from -8 times the limb sum (row r + 8:
-                            // 16 u, hence -128 times)
+                for (int kk = 0; kk < 2; ++kk) {
+                    const int k32 = 2 * k64 + kk;
+                    if (k32 % (4 / SUB) == 0) {
+                        // a group starts from -8 times the limb sum (row r + 8:
+                        // 16 u, hence -128 times)
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    const uint32_t v = sum[n][j][k32 / (4 / SUB)];
-                                    const int32_t hi = static_cast<int32_t>(v) >> 16;
-                                    const int32_t lo = static_cast<int16_t>(v & 0xffffu);
+                            for (int j = 0; j < 2; ++j) {
+                                const uint32_t v = sum[n][j][k32 / (4 / SUB)];
+                                const int32_t hi = static_cast<int32_t>(v) >> 16;
+                                const int32_t lo = static_cast<int16_t>(v & 0xffffu);
 #pragma unroll
-                                    for (int h = 0; h < 2; ++h) {
-                                        acc[0][h][n][j] = kW4MagicBits - 8 * hi;
-                                        acc[0][h][n][2 + j] = kW4MagicBits - 128 * hi;
-                                        acc[1][h][n][j] = kW4MagicBits - 8 * lo;
-                                        acc[1][h][n][2 + j] = kW4MagicBits - 128 * lo;
-                                    }
+                                for (int h = 0; h < 2; ++h) {
+                                    acc[0][h][n][j] = kW4MagicBits - 8 * hi;
+                                    acc[0][h][n][2 + j] = kW4MagicBits - 128 * hi;
+                                    acc[1][h][n][j] = kW4MagicBits - 8 * lo;
+                                    acc[1][h][n][2 + j] = kW4MagicBits - 128 * lo;
                                 }
-                        }
+                            }
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t w0 = s.a[h][2 * k32], w1 = s.a[h][2 * k32 + 1];
+                        const uint32_t f[4] = {w0 & 0x0f0f0f0fu, w0 & 0xf0f0f0f0u,
+                                               w1 & 0x0f0f0f0fu, w1 & 0xf0f0f0f0u};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int l = 0; l < 2; ++l)
+                                mma_u8s8(acc[l][h][n], f, kk ? bv[n][l].z : bv[n][l].x,
+                                         kk ? bv[n][l].w : bv[n][l].y);
+                    }
+                    if ((k32 + 1) % (4 / SUB) == 0) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint32_t w0 = s.a[h][2 * k32], w1 = s.a[h][2 * k32 + 1];
-                            const uint32_t f[4] = {w0 & 0x0f0f0f0fu, w0 & 0xf0f0f0f0u,
-                                                   w1 & 0x0f0f0f0fu, w1 & 0xf0f0f0f0u};
+                            const uint2 s2 = s.s[k32 / (4 / SUB)];
+                            const uint32_t sw = h ? s2.y : s2.x;
+                            const float2 sv = __bfloat1622float2(
+                                *reinterpret_cast<const __nv_bfloat162*>(&sw));
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                                for (int l = 0; l < 2; ++l)
-                                    mma_u8s8(acc[l][h][n], f, kk ? bv[n][l].z : bv[n][l].x,
-                                             kk ? bv[n][l].w : bv[n][l].y);
-                        }
-                        if ((k32 + 1) % (4 / SUB) == 0) {
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint2 s2 = s.s[k32 / (4 / SUB)];
-                                const uint32_t sw = h ? s2.y : s2.x;
-                                const float2 sv = __bfloat1622float2(
-                                    *reinterpret_cast<const __nv_bfloat162*>(&sw));
-#pragma unroll
-                                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const float hi = __int_as_float(acc[0][h][n][i]) - kW4Magic;
-                                        const float lo = __int_as_float(acc[1][h][n][i]) - kW4Magic;
-                                        tot[h][n][i] = fmaf((i < 2 ? sv.x : sv.y) * scale[n][i & 1],
-                                                            fmaf(256.0f, hi, lo), tot[h][n][i]);
-                                    }
-                            }
+                                for (int i = 0; i < 4; ++i) {
+                                    const float hi = __int_as_float(acc[0][h][n][i]) - kW4Magic;
+                                    const float lo = __int_as_float(acc[1][h][n][i]) - kW4Magic;
+                                    tot[h][n][i] = fmaf((i < 2 ? sv.x : sv.y) * scale[n][i & 1],
+                                                        fmaf(256.0f, hi, lo), tot[h][n][i]);
+                                }
                         }
                     }
                 }
+            }
 #pragma unroll
-                for (int n = 0; n < NT; ++n) b[n] += kW4RowBlock;
-            };
+            for (int n = 0; n < NT; ++n) b[n] += cap * kW4RowBytes;
+        };
 #pragma unroll 1
-            for (int kb = kb0; kb < kb1; kb += 2) {
-                block(st[0]);
-                load(st[0], kb + 2);
-                if (kb + 1 < kb1) {
-                    block(st[1]);
-                    load(st[1], kb + 3);
+        for (int kb = kb0; kb < kb1; kb += kStages) {
+#pragma unroll
+            for (int i = 0; i < kStages; ++i) {
+                if (kb + i < kb1) {
+                    block(st[i]);
+                    load(st[i], kb + i + kStages);
                 }
             }
         }
-        float* sums = s_sum[round & 1][warp];
+        float* sums = s_sum[buffer][warp];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sums[((h * NT + n) * 4 + i) * 32 + lane] = tot[h][n][i];
-        // the next tile's first blocks are on their way before this one is added up
-        const W4Place cur = at;
-        if (round + 1 < tasks) {
-            for (int i = 0; i < per_cta; ++i) w4_advance(at, sp, args.nseg, args.tiles);
-            first_blocks();
+        // the next round's first weights are on their way before this one is
+        // added up, and its rows while it is
+        W4Round next = cur;
+        const bool more = cur.left > 0;
+        const int cur_slot = slot, part = warp & ((1 << cur.log_ks) - 1);
+        if (more) {
+            w4_next_round<kWarps>(next, sp, args.tiles, args.nseg, base, most);
+            first_blocks(next);
         }
-        // (two buffers in turn: the barrier of the next round lies between this
-        // round's reads and the writes of the round after)
+        const bool other_rows = next.seg != cur.seg || next.chunk != cur.chunk;
+        // (two buffers of sums in turn: the barrier of the next round lies between
+        // this round's reads and the writes of the round after)
         __syncthreads();
-        if (!mine) continue;
-        // lane 4r + c, value i: row r + 8 (i / 2) of half h, column 8n + 2c + i % 2
-        const float(*from)[kVals] = &s_sum[round & 1][slot * ks];
-        constexpr int kOut = DOWN ? kVals : kVals / 2;
-        for (int v = part * 32 + lane; v < kOut; v += ks * 32) {
-            const int i = (v >> 5) & 3, n = (v >> 7) % NT, h = v / (kVals / 2);
-            const int col = 8 * n + 2 * c + (i & 1);
-            if (col >= nrows) continue;
-            float g = 0.0f, u = 0.0f;
-            for (int w = 0; w < ks; ++w) {
-                g += from[w][v];
-                if constexpr (!DOWN) u += from[w][v + kVals / 2];
-            }
-            const int64_t row = sp.out_row0[cur.seg] + row0 + col;
-            if constexpr (!DOWN) {
+        if (more && other_rows) fetch_rows(next);
+        if (cur_slot < cur.tiles) {
+            // lane 4r + c, value i: row r + 8 (i / 2) of half h, column 8n + 2c + i % 2
+            const int ks = 1 << cur.log_ks, tile = cur.tile + cur_slot;
+            const float(*from)[kVals] = &s_sum[buffer][cur_slot << cur.log_ks];
+            constexpr int kOut = DOWN ? kVals : kVals / 2;
+            for (int v = part * 32 + lane; v < kOut; v += ks * 32) {
+                const int i = (v >> 5) & 3, n = (v >> 7) % NT, h = v / (kVals / 2);
+                const int col = 8 * n + 2 * c + (i & 1);
+                if (col >= nrows) continue;
+                float g = 0.0f, u = 0.0f;
+                for (int w = 0; w < ks; ++w) {
+                    g += from[w][v];
+                    if constexpr (!DOWN) u += from[w][v + kVals / 2];
+                }
+                const int64_t row = sp.out_row0[cur.seg] + row0 + col;
                 if (i >= 2) {  // row r + 8 carries 16 u
                     g *= 0.0625f;
                     u *= 0.0625f;
                 }
-                // compare-select clamp: NaN passes through
-                g = g > args.clip ? args.clip : (g < -args.clip ? -args.clip : g);
-                u = u > args.clip ? args.clip : (u < -args.clip ? -args.clip : u);
-                args.out[row * args.ld + cur.tile * 16 + (i >> 1) * 8 + r] =
-                    g / (1.0f + __expf(-g)) * u;
-            } else {
-                const float wt = row < args.routed_rows ? args.row_w[row] : 1.0f;
-                args.out[row * args.ld + cur.tile * 32 + h * 16 + (i >> 1) * 8 + r] =
-                    wt * (i >= 2 ? 0.0625f * g : g);
+                if constexpr (!DOWN) {
+                    // compare-select clamp: NaN passes through
+                    g = g > args.clip ? args.clip : (g < -args.clip ? -args.clip : g);
+                    u = u > args.clip ? args.clip : (u < -args.clip ? -args.clip : u);
+                    args.out[row * args.ld + tile * 16 + (i >> 1) * 8 + r] =
+                        g / (1.0f + __expf(-g)) * u;
+                } else {
+                    const float wt = row < args.routed_rows ? args.row_w[row] : 1.0f;
+                    args.out[row * args.ld + tile * 32 + h * 16 + (i >> 1) * 8 + r] = wt * g;
+                }
             }
         }
+        if (!more) break;
+        if (other_rows) {
+            ptx::cp_async_wait_all();
+            __syncthreads();
+        }
+        cur = next;
     }
 }
 
@@ -451,15 +538,16 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1)
 // the token rows into limbs meanwhile.
 __global__ void __launch_bounds__(512) w4_dispatch_kernel(
     const int32_t* __restrict__ idx, const float* __restrict__ topk_w, int T, int E, int k,
-    int num_shared, int nmax, int32_t* sched_gu, int32_t* sched_dn, int32_t* __restrict__ pos,
+    int num_shared, int32_t* sched_gu, int nmax_gu, int32_t* sched_dn, int nmax_dn,
+    int32_t* __restrict__ pos,
     int32_t* __restrict__ src, float* __restrict__ row_w, int32_t* status,
     const __nv_bfloat16* __restrict__ x, int64_t units, int sub,
-    uint8_t* __restrict__ row_blocks) {
+    uint8_t* __restrict__ limbs, uint32_t* __restrict__ meta) {
     if (blockIdx.x > 0) {
         ptx::grid_dep_wait();
         ptx::grid_dep_launch();
         const int64_t unit = (static_cast<int64_t>(blockIdx.x) - 1) * 16 + (threadIdx.x >> 5);
-        if (unit < units) w4_split_block<__nv_bfloat16>(x, sub, unit, row_blocks);
+        if (unit < units) w4_split_block<__nv_bfloat16>(x, sub, unit, limbs, meta);
         return;
     }
     __shared__ uint32_t masks[kPermWarps][kMaxExperts];
@@ -489,12 +577,13 @@ __global__ void __launch_bounds__(512) w4_dispatch_kernel(
     const int nseg = E + num_shared;
     const bool shared = num_shared && tid == E;
     const int rows = tid < E ? cnt : (shared ? T : 0);
-    int total = 0;
-    const int pre = block_exclusive_scan((rows + nmax - 1) / nmax, s_warp, &total);
-    if (tid < nseg) {
-        const int o0 = shared ? T * k : off;
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
+    for (int which = 0; which < 2; ++which) {
+        const int nmax = which == 0 ? nmax_gu : nmax_dn;
+        int total = 0;
+        const int pre = block_exclusive_scan((rows + nmax - 1) / nmax, s_warp, &total);
+        if (tid < nseg) {
+            const int o0 = shared ? T * k : off;
             const SchedPtrs sp = sched_ptrs(which == 0 ? sched_gu : sched_dn, nseg);
             const_cast<int32_t*>(sp.prefix)[tid] = pre;
             const_cast<int32_t*>(sp.b_row0)[tid] = shared && which == 0 ? 0 : o0;
