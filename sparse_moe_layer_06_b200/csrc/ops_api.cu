@@ -170,12 +170,12 @@ int32_t launch_w4_n(const W4Args& a, int64_t max_tasks, cudaStream_t s) {
     static std::atomic<uint64_t> configured{0};
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
     if (!bit || !(configured.load() & bit)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024) !=
             cudaSuccess)
             return MOE_ERR_CUDA;
         configured.fetch_or(bit);
     }
-    const int smem = W4Shape<NT>::kSumBytes +
+    const int smem = 2 * W4Shape<NT>::kSumBytes + W4Shape<NT>::kSlack +
                      a.K / kW4Block * a.cap * (kW4RowBytes + 4 * w4_meta_words(SUB));
     const int grid =
         static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sm_count(), max_tasks)));

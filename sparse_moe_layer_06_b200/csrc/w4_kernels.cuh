@@ -12,10 +12,9 @@
 // limbs: bf16 values down to 2^-7 of the block's largest are exact, smaller ones
 // off by at most a / 2, 2^-15 of the largest, far inside the bf16 output's
 // rounding.  With the sums of the limbs of each group,
-//   sum_k (u_k - 8) s x_k = s a (256 (sum u hi - 8 sum hi) + (sum u lo - 8 sum lo)),
-// and an accumulator that starts from the bits of 1.5 * 2^23 less 8 times the
-// limb sum ends as the fp32 number 1.5 * 2^23 + sum (u - 8) limb: the result is
-// below 2^22, so no conversion is needed.
+//   sum_k (u_k - 8) s x_k = s a (256 (sum u hi - 8 sum hi) + (sum u lo - 8 sum lo)):
+// the accumulators start from -8 times the limb sums, and the joined integer,
+// below 2^29, is converted, scaled and added to the fp32 total once per group.
 //
 // Layout.  Each matrix (gate/up: rows i of both, contraction H; down: rows h,
 // contraction I) is cut into pair tiles of 2 x 16 rows (gate/up: 16 gate rows
@@ -45,26 +44,31 @@ constexpr int kW4BlockBytes = 2048; // codes of a pair tile's block
 constexpr int kW4RowBytes = 256;    // limbs of a row's block
 constexpr int kW4MaxK = 65536;      // longest contraction (a row's limbs: 147 KB)
 
-// Shape of a launch whose tasks have up to 8 NT rows: warps of a CTA (one CTA
-// per SM) and weight blocks that each warp has on the way in registers.  One
-// column tile leaves 128 registers a thread and so 16 warps; two take more.
+// Shape of a launch whose tasks have up to 8 NT rows: one CTA per SM.  One column
+// tile leaves 128 registers a thread and so 16 warps, two take up to 168.
 template <int NT>
 struct W4Shape {
-    static constexpr int kWarps = NT == 1 ? 16 : 8;
-    static constexpr int kStages = NT == 1 ? 2 : 3;
-    static constexpr int kVals = 2 * NT * 4 * 32;             // fp32 sums of a tile
-    static constexpr int kSumBytes = 2 * kWarps * kVals * 4;  // two buffers of them
+    static constexpr int kWarps = NT == 1 ? 16 : 12;
+    static constexpr int kMostLog = NT == 1 ? 4 : 2;  // log2 of the warps that share a tile
+    static constexpr int kStages = 2;  // weight blocks a warp has on the way in registers
+    static constexpr int kAhead = 6;   // blocks that L2 has on the way for it
+    static constexpr int kVals = 2 * NT * 4 * 32;         // fp32 sums of a tile
+    static constexpr int kSumBytes = kWarps * kVals * 4;  // a buffer of them
+    static constexpr int kSlack = 8 * NT * kW4RowBytes;   // rows read past the last block
 };
 
-// Words per row and block of the group sums and the scale, for SUB groups.
-__host__ __device__ constexpr int w4_meta_words(int sub) { return sub == 1 ? 2 : (sub == 2 ? 4 : 8); }
+// Sums of the token rows' limbs are kept for groups of at most 64 values, so a
+// block has w4_sums of them; words per row and block of the sums and the scale.
+__host__ __device__ constexpr int w4_sums(int sub) { return sub == 4 ? 4 : 2; }
+__host__ __device__ constexpr int w4_meta_words(int sub) { return sub == 4 ? 8 : 4; }
 constexpr int kW4MaxMeta = 8;
 
-// Rows of K values that fit beside the sums in a CTA's shared memory, at most 8 NT.
+// Rows of K values that fit beside the sums and the schedule (4 KB) in a CTA's
+// shared memory, at most 8 NT.
 template <int NT>
 int w4_rows_cap(int64_t K, int sub) {
     const int64_t row = K / kW4Block * (kW4RowBytes + 4 * w4_meta_words(sub));
-    const int64_t cap = (227 * 1024 - W4Shape<NT>::kSumBytes) / row;
+    const int64_t cap = (222 * 1024 - 2 * W4Shape<NT>::kSumBytes - W4Shape<NT>::kSlack) / row;
     return static_cast<int>(cap < 8 * NT ? cap : 8 * NT);
 }
 
@@ -87,17 +91,16 @@ struct W4Args {
     float clip;
 };
 
+// d = c + a b
 __device__ __forceinline__ void mma_u8s8(int32_t (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
+                                         uint32_t b1, const int32_t (&c)[4]) {
     asm volatile(
         "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]),
+          "r"(c[2]), "r"(c[3]));
 }
-
-constexpr int32_t kW4MagicBits = 0x4b400000;   // 1.5 * 2^23 as fp32
-constexpr float kW4Magic = 12582912.0f;
 
 // 32 bytes that are read once: past L1, first to leave L2.
 __device__ __forceinline__ void ldg_stream(const void* p, uint32_t (&v)[8]) {
@@ -106,6 +109,11 @@ __device__ __forceinline__ void ldg_stream(const void* p, uint32_t (&v)[8]) {
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
           "=r"(v[7])
         : "l"(p));
+}
+
+// Brings bytes (a multiple of 16, 16-byte aligned) on their way into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // The codes and scales of one block of a pair tile, as one lane holds them.
@@ -169,7 +177,7 @@ __device__ __forceinline__ void w4_split_block(const T* __restrict__ rows, int s
     }
     *reinterpret_cast<uint32_t*>(out) = hi;
     *reinterpret_cast<uint32_t*>(out + 64) = lo;
-    const int per = 32 / sub;  // lanes of a group
+    const int sums = w4_sums(sub), per = 32 / sums;  // lanes of a group
     for (int o = 1; o < per; o <<= 1) {
         sum_hi += __shfl_xor_sync(0xffffffffu, sum_hi, o);
         sum_lo += __shfl_xor_sync(0xffffffffu, sum_lo, o);
@@ -177,7 +185,7 @@ __device__ __forceinline__ void w4_split_block(const T* __restrict__ rows, int s
     if (lane % per == 0)
         meta[lane / per] = (static_cast<uint32_t>(sum_hi) << 16) |
                            (static_cast<uint32_t>(sum_lo) & 0xffffu);
-    if (lane == 0) meta[sub] = bad ? 0x7fc00000u : __float_as_uint(scale);
+    if (lane == 0) meta[sums] = bad ? 0x7fc00000u : __float_as_uint(scale);
 }
 
 template <typename T>
@@ -190,40 +198,46 @@ __global__ void __launch_bounds__(256) w4_split_kernel(const T* __restrict__ row
     if (unit < units) w4_split_block<T>(rows, sub, unit, out, meta);
 }
 
-// A round of a CTA: `tiles` tiles from `tile` on of one chunk of rows, each
-// shared by 2^log_ks warps.
-struct W4Round {
-    int seg, chunk;   // segment, and chunk within it
-    int tile, tiles;
-    int log_ks;
-    int left;         // tasks of the CTA behind this round
+// The tile schedule in shared memory.
+struct W4Sched {
+    int32_t prefix[kMaxSegments + 1], b_row0[kMaxSegments], out_row0[kMaxSegments],
+        rows[kMaxSegments];
 };
 
-// Segment of chunk g of the launch: the last whose first chunk is not behind it.
-__device__ __forceinline__ int w4_segment(const SchedPtrs& sp, int nseg, int g) {
+// A round of a CTA: `tiles` tiles from `tile` on of one chunk of rows (chunk
+// number `group` of the launch), each shared by 2^log_ks warps.
+struct W4Round {
+    int group, seg, row0, nrows;  // the chunk's segment and rows of it
+    int tile, tiles;
+    int log_ks;
+    int left;  // tasks of the CTA behind this round
+};
+
+// Segment and rows of chunk p.group: the segment is the last whose first chunk
+// is not behind it.
+__device__ __forceinline__ void w4_find_chunk(W4Round& p, const W4Sched& sp, int nseg, int cap) {
     int lo = 0, hi = nseg - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (sp.prefix[mid] <= g) lo = mid;
+        if (sp.prefix[mid] <= p.group) lo = mid;
         else hi = mid - 1;
     }
-    return lo;
+    p.seg = lo;
+    p.row0 = (p.group - sp.prefix[lo]) * cap;
+    p.nrows = min(cap, sp.rows[lo] - p.row0);
 }
 
 // The round behind `p` (p.tiles = 0: the first one, p.tile its tile): as many
 // tiles as the warps hold at 2^base warps each, or, for fewer tiles than that,
 // as many as keep all warps busy.
 template <int kWarps>
-__device__ __forceinline__ void w4_next_round(W4Round& p, const SchedPtrs& sp, int all_tiles,
-                                              int nseg, int base, int most) {
+__device__ __forceinline__ void w4_next_round(W4Round& p, const W4Sched& sp, int all_tiles,
+                                              int nseg, int cap, int base, int most) {
     p.tile += p.tiles;
     if (p.tile == all_tiles) {
         p.tile = 0;
-        if (sp.prefix[p.seg] + ++p.chunk == sp.prefix[p.seg + 1]) {
-            p.chunk = 0;
-            do ++p.seg;
-            while (p.seg + 1 < nseg && sp.prefix[p.seg] == sp.prefix[p.seg + 1]);
-        }
+        ++p.group;
+        w4_find_chunk(p, sp, nseg, cap);
     }
     const int rem = min(all_tiles - p.tile, p.left);
     int l = base;
@@ -240,7 +254,8 @@ __device__ __forceinline__ void w4_next_round(W4Round& p, const SchedPtrs& sp, i
 // cost more than the weights, 700 against 456 us for the gate/up weights of 222
 // experts (2.9 GB).  2^log_ks warps share a tile, each with a part of its
 // blocks; their fp32 sums are added in shared memory in warp order.  The weights
-// stream through registers, kStages blocks ahead and across rounds, past L1.
+// stream through registers, kStages blocks ahead and across rounds, past L1; that
+// covers the way from L2, and a prefetch kAhead blocks further that from memory.
 template <int NT, bool DOWN, int SUB>
 __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
     w4_product_kernel(const W4Args args) {
@@ -249,14 +264,26 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
     constexpr int kMeta = w4_meta_words(SUB);
     extern __shared__ __align__(128) uint8_t s_dyn[];
     float(*s_sum)[kWarps][kVals] = reinterpret_cast<float(*)[kWarps][kVals]>(s_dyn);
-    uint8_t* s_rows = s_dyn + S::kSumBytes;  // [block][cap rows][256]
+    uint8_t* s_rows = s_dyn + 2 * S::kSumBytes;  // [block][cap rows][256]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, c = lane & 3;
     const int nkb = args.K / kW4Block, cap = args.cap;
     uint32_t* s_meta = reinterpret_cast<uint32_t*>(s_rows + nkb * cap * kW4RowBytes);
-    const SchedPtrs sp = sched_ptrs(args.sched, args.nseg);
+    __shared__ W4Sched sp;
     if constexpr (!DOWN) ptx::grid_dep_wait();
     ptx::grid_dep_launch();
+    {
+        const SchedPtrs from = sched_ptrs(args.sched, args.nseg);
+        for (int i = threadIdx.x; i <= args.nseg; i += kWarps * 32) {
+            sp.prefix[i] = from.prefix[i];
+            if (i < args.nseg) {
+                sp.b_row0[i] = from.b_row0[i];
+                sp.out_row0[i] = from.out_row0[i];
+                sp.rows[i] = from.rows[i];
+            }
+        }
+    }
+    __syncthreads();
     // this CTA's run of tasks
     const int groups = sp.prefix[args.nseg];
     const int64_t total = static_cast<int64_t>(groups) * args.tiles;
@@ -269,7 +296,7 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
     // warps per tile: the fewest blocks on any warp's way, a round counting as
     // two more for its barrier and sums
     int most = 0, base = 0;
-    while ((2 << most) <= min(kWarps, nkb)) ++most;
+    while (most < S::kMostLog && (2 << most) <= nkb) ++most;
     for (int l = 0, best = 0x7fffffff; l <= most; ++l) {
         const int cost = ((run + (kWarps >> l) - 1) / (kWarps >> l)) * (((nkb - 1) >> l) + 3);
         if (cost < best) {
@@ -278,26 +305,41 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
         }
     }
 
-    W4Round cur{};
+    W4Round cur{}, next{};
     {
-        const int g = static_cast<int>(begin / args.tiles);
-        cur.seg = w4_segment(sp, args.nseg, g);
-        cur.chunk = g - sp.prefix[cur.seg];
-        cur.tile = static_cast<int>(begin - static_cast<int64_t>(g) * args.tiles);
+        cur.group = static_cast<int>(begin / args.tiles);
+        cur.tile = static_cast<int>(begin - static_cast<int64_t>(cur.group) * args.tiles);
         cur.left = run;
-        w4_next_round<kWarps>(cur, sp, args.tiles, args.nseg, base, most);
+        w4_find_chunk(cur, sp, args.nseg, cap);
+        w4_next_round<kWarps>(cur, sp, args.tiles, args.nseg, cap, base, most);
     }
-    // the warp's part of a round: tile slot, blocks [kb0, kb1)
-    int slot = 0, kb0 = 0, kb1 = 0;
-    const uint8_t* q = nullptr;
-    const uint8_t* sc = nullptr;
+    // the warp's part of a round: n blocks, its tile's codes and scales from the
+    // first of them on
+    struct Part {
+        const uint8_t* q;
+        const uint8_t* sc;
+        int n;
+    };
+    auto part_of = [&](const W4Round& p) {
+        const int slot = warp >> p.log_ks, part = warp & ((1 << p.log_ks) - 1);
+        const int kb0 = part * nkb >> p.log_ks;
+        const bool special = p.seg == args.special;
+        const int64_t unit = static_cast<int64_t>(p.tile + slot) * nkb + kb0;
+        Part w;
+        w.q = (special ? args.q_shared : args.q + p.seg * args.q_stride) + unit * kW4BlockBytes;
+        w.sc = reinterpret_cast<const uint8_t*>(
+                   special ? args.sc_shared : args.sc + p.seg * args.sc_stride) +
+               unit * 64 * SUB;
+        w.n = slot < p.tiles ? ((part + 1) * nkb >> p.log_ks) - kb0 : 0;
+        return w;
+    };
     W4Stage<SUB> st[kStages];
-    auto load = [&](W4Stage<SUB>& s, int kb) {
-        if (kb < kb1) {
-            const uint8_t* p = q + static_cast<int64_t>(kb) * kW4BlockBytes;
+    auto load = [&](W4Stage<SUB>& s, const Part& w, int i) {
+        if (i < w.n) {
+            const uint8_t* p = w.q + static_cast<int64_t>(i) * kW4BlockBytes + lane * 32;
             ldg_stream(p, s.a[0]);
             ldg_stream(p + 1024, s.a[1]);
-            p = sc + static_cast<int64_t>(kb) * 64 * SUB;
+            p = w.sc + static_cast<int64_t>(i) * 64 * SUB + r * 8 * SUB;
             if constexpr (SUB == 1) {
                 s.s[0] = __ldg(reinterpret_cast<const uint2*>(p));
             } else {
@@ -310,27 +352,18 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
             }
         }
     };
-    auto first_blocks = [&](const W4Round& p) {
-        const int part = warp & ((1 << p.log_ks) - 1);
-        slot = warp >> p.log_ks;
-        kb0 = part * nkb >> p.log_ks;
-        kb1 = slot < p.tiles ? (part + 1) * nkb >> p.log_ks : kb0;
-        const bool special = p.seg == args.special;
-        const int64_t unit = static_cast<int64_t>(p.tile + slot) * nkb;
-        q = (special ? args.q_shared : args.q + p.seg * args.q_stride) + unit * kW4BlockBytes +
-            lane * 32;
-        sc = reinterpret_cast<const uint8_t*>(
-            (special ? args.sc_shared : args.sc + p.seg * args.sc_stride) +
-            (unit * 8 + r) * SUB * 4);
-#pragma unroll
-        for (int i = 0; i < kStages; ++i) load(st[i], kb0 + i);
+    auto prefetch = [&](const Part& w, int i) {
+        if (i < w.n && lane == 0) {
+            prefetch_l2(w.q + static_cast<int64_t>(i) * kW4BlockBytes, kW4BlockBytes);
+            prefetch_l2(w.sc + static_cast<int64_t>(i) * 64 * SUB, 64 * SUB);
+        }
     };
+    Part mine = part_of(cur), then{};
     // the chunk's rows into shared memory (asynchronous copies of this thread)
     auto fetch_rows = [&](const W4Round& p) {
-        const int row0 = p.chunk * cap, nrows = min(cap, sp.rows[p.seg] - row0);
-        const int first = sp.b_row0[p.seg] + row0;
+        const int first = sp.b_row0[p.seg] + p.row0;
         const bool direct = DOWN || p.seg == args.special;
-        for (int row = warp; row < nrows; row += kWarps) {
+        for (int row = warp; row < p.nrows; row += kWarps) {
             const int64_t m = (direct ? first + row : args.row_src[first + row]);
             const uint8_t* src = args.rows + m * nkb * kW4RowBytes;
             for (int i = lane; i < nkb * 16; i += 32)
@@ -342,15 +375,21 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
                 s_meta[((i / kMeta) * cap + row) * kMeta + i % kMeta] = meta[i];
         }
     };
-    first_blocks(cur);
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) load(st[i], mine, i);
+    for (int i = kStages; i < kStages + S::kAhead; ++i) prefetch(mine, i);
     if constexpr (DOWN) ptx::grid_dep_wait();  // (the weights and the schedule are older)
     fetch_rows(cur);
     ptx::cp_async_wait_all();
     __syncthreads();
 
     for (int buffer = 0;; buffer ^= 1) {
-        const int row0 = cur.chunk * cap;
-        const int nrows = min(cap, sp.rows[cur.seg] - row0);
+        const bool more = cur.left > 0;
+        if (more) {
+            next = cur;
+            w4_next_round<kWarps>(next, sp, args.tiles, args.nseg, cap, base, most);
+            then = part_of(next);
+        }
         float tot[2][NT][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -358,115 +397,127 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tot[h][n][i] = 0.0f;
-        // the lane's row of each 8 (those past the last repeat it, not stored),
-        // and its columns' sums and scales
-        uint32_t b[NT], m[NT][2];  // offsets into s_rows and s_meta
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int row = min(8 * n + r, nrows - 1);
-            b[n] = (kb0 * cap + row) * kW4RowBytes + (c ^ ((row & 1) * 4)) * 16;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                m[n][j] = (kb0 * cap + min(8 * n + 2 * c + j, nrows - 1)) * kMeta;
-        }
+        // offsets of the lane's row r and of its columns' sums and scales (rows
+        // past the chunk's last hold anything: their columns are not stored)
+        const int kb0 = (warp & ((1 << cur.log_ks) - 1)) * nkb >> cur.log_ks;
+        uint32_t b = (kb0 * cap + r) * kW4RowBytes + (c ^ ((r & 1) * 4)) * 16;
+        uint32_t m = (kb0 * cap + 2 * c) * kMeta;
         auto block = [&](const W4Stage<SUB>& s) {
-            uint32_t sum[NT][2][SUB];
+            constexpr int kSums = w4_sums(SUB);
+            // with one column tile the two halves' accumulators of a whole block
+            // fit; with two, groups of at most 64 run one half after the other
+            constexpr bool kWhole = NT == 1 && SUB == 1;
+            uint32_t sum[NT][2][kSums];
             float scale[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    if constexpr (SUB == 1) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(s_meta + m[n][j]);
-                        sum[n][j][0] = v.x;
-                        scale[n][j] = __uint_as_float(v.y);
-                    } else {
-                        const uint4 v = *reinterpret_cast<const uint4*>(s_meta + m[n][j]);
-                        sum[n][j][0] = v.x;
-                        sum[n][j][1] = v.y;
-                        if constexpr (SUB == 4) {
-                            sum[n][j][2] = v.z;
-                            sum[n][j][3] = v.w;
-                        }
-                        scale[n][j] = __uint_as_float(SUB == 2 ? v.z : s_meta[m[n][j] + 4]);
+                    const uint32_t* p = s_meta + m + (8 * n + j) * kMeta;
+                    const uint4 v = *reinterpret_cast<const uint4*>(p);
+                    sum[n][j][0] = v.x;
+                    sum[n][j][1] = v.y;
+                    if constexpr (SUB == 4) {
+                        sum[n][j][2] = v.z;
+                        sum[n][j][3] = v.w;
                     }
-                    m[n][j] += cap * kMeta;
+                    scale[n][j] = __uint_as_float(SUB == 4 ? p[4] : v.z);
                 }
-            int32_t acc[2][2][NT][4];  // [limb hi, lo][half]
+            m += cap * kMeta;
+            int32_t acc[kWhole ? 2 : 1][2][NT][4];  // [half][limb hi, lo]
+            int32_t from[2][NT][4];  // -8 times the limb sums (row r + 8: 16 u, -128)
+            auto start = [&](int g) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t v = sum[n][j][g];
+                        int32_t hi = static_cast<int32_t>(v) >> 16;
+                        int32_t lo = static_cast<int16_t>(v & 0xffffu);
+                        if constexpr (kWhole) {
+                            hi += static_cast<int32_t>(sum[n][j][1]) >> 16;
+                            lo += static_cast<int16_t>(sum[n][j][1] & 0xffffu);
+                        }
+                        from[0][n][j] = -8 * hi;
+                        from[0][n][2 + j] = -128 * hi;
+                        from[1][n][j] = -8 * lo;
+                        from[1][n][2 + j] = -128 * lo;
+                    }
+            };
+            auto finish = [&](const int32_t (&a)[2][NT][4], int h, int g) {
+                const uint2 s2 = s.s[g];
+                const uint32_t sw = h ? s2.y : s2.x;
+                const float2 sv = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&sw));
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tot[h][n][i] = fmaf((i < 2 ? sv.x : sv.y) * scale[n][i & 1],
+                                            static_cast<float>(a[0][n][i] * 256 + a[1][n][i]),
+                                            tot[h][n][i]);
+            };
+            uint4 bv[NT][2];
+            auto step = [&](int32_t (&a)[2][NT][4], int h, int k32, bool first) {
+                const uint32_t w0 = s.a[h][2 * k32], w1 = s.a[h][2 * k32 + 1];
+                const uint32_t f[4] = {w0 & 0x0f0f0f0fu, w0 & 0xf0f0f0f0u, w1 & 0x0f0f0f0fu,
+                                       w1 & 0xf0f0f0f0u};
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int l = 0; l < 2; ++l)
+                        mma_u8s8(a[l][n], f, (k32 & 1) ? bv[n][l].z : bv[n][l].x,
+                                 (k32 & 1) ? bv[n][l].w : bv[n][l].y,
+                                 first ? from[l][n] : a[l][n]);
+            };
+            if constexpr (kWhole) start(0);
 #pragma unroll
             for (int k64 = 0; k64 < 2; ++k64) {
-                uint4 bv[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int l = 0; l < 2; ++l)
                         // (piece 8 k64 + 4 l + c, its bit 2 flipped in odd rows)
-                        bv[n][l] = *reinterpret_cast<const uint4*>(s_rows + (b[n] ^ (l * 64)) +
-                                                                   k64 * 128);
+                        bv[n][l] = *reinterpret_cast<const uint4*>(
+                            s_rows + (b ^ (l * 64)) + k64 * 128 + n * 8 * kW4RowBytes);
+                if constexpr (kWhole) {
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    const int k32 = 2 * k64 + kk;
-                    if (k32 % (4 / SUB) == 0) {
-                        // a group starts from -8 times the limb sum (row r + 8:
-                        // 16 u, hence -128 times)
+                    for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
+                        for (int h = 0; h < 2; ++h)
+                            step(acc[h], h, 2 * k64 + kk, 2 * k64 + kk == 0);
+                } else {
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const uint32_t v = sum[n][j][k32 / (4 / SUB)];
-                                const int32_t hi = static_cast<int32_t>(v) >> 16;
-                                const int32_t lo = static_cast<int16_t>(v & 0xffffu);
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    acc[0][h][n][j] = kW4MagicBits - 8 * hi;
-                                    acc[0][h][n][2 + j] = kW4MagicBits - 128 * hi;
-                                    acc[1][h][n][j] = kW4MagicBits - 8 * lo;
-                                    acc[1][h][n][2 + j] = kW4MagicBits - 128 * lo;
-                                }
-                            }
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t w0 = s.a[h][2 * k32], w1 = s.a[h][2 * k32 + 1];
-                        const uint32_t f[4] = {w0 & 0x0f0f0f0fu, w0 & 0xf0f0f0f0u,
-                                               w1 & 0x0f0f0f0fu, w1 & 0xf0f0f0f0u};
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int l = 0; l < 2; ++l)
-                                mma_u8s8(acc[l][h][n], f, kk ? bv[n][l].z : bv[n][l].x,
-                                         kk ? bv[n][l].w : bv[n][l].y);
-                    }
-                    if ((k32 + 1) % (4 / SUB) == 0) {
+                    for (int g = 0; g < (SUB == 4 ? 2 : 1); ++g) {
+                        start(SUB == 4 ? 2 * k64 + g : k64);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint2 s2 = s.s[k32 / (4 / SUB)];
-                            const uint32_t sw = h ? s2.y : s2.x;
-                            const float2 sv = __bfloat1622float2(
-                                *reinterpret_cast<const __nv_bfloat162*>(&sw));
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float hi = __int_as_float(acc[0][h][n][i]) - kW4Magic;
-                                    const float lo = __int_as_float(acc[1][h][n][i]) - kW4Magic;
-                                    tot[h][n][i] = fmaf((i < 2 ? sv.x : sv.y) * scale[n][i & 1],
-                                                        fmaf(256.0f, hi, lo), tot[h][n][i]);
-                                }
+                            if constexpr (SUB == 4) {
+                                step(acc[0], h, 2 * k64 + g, true);
+                            } else {
+                                step(acc[0], h, 2 * k64, true);
+                                step(acc[0], h, 2 * k64 + 1, false);
+                            }
+                            finish(acc[0], h, SUB == 4 ? 2 * k64 + g : (SUB == 2 ? k64 : 0));
                         }
                     }
                 }
             }
+            if constexpr (kWhole) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) b[n] += cap * kW4RowBytes;
+                for (int h = 0; h < 2; ++h) finish(acc[h], h, 0);
+            }
+            b += cap * kW4RowBytes;
         };
 #pragma unroll 1
-        for (int kb = kb0; kb < kb1; kb += kStages) {
+        for (int kb = 0; kb < mine.n; kb += kStages) {
 #pragma unroll
             for (int i = 0; i < kStages; ++i) {
-                if (kb + i < kb1) {
+                if (kb + i < mine.n) {
+                    const int ahead = kb + i + kStages + S::kAhead;
+                    if (ahead < mine.n) prefetch(mine, ahead);
+                    else if (more) prefetch(then, ahead - mine.n);
                     block(st[i]);
-                    load(st[i], kb + i + kStages);
+                    load(st[i], mine, kb + i + kStages);
                 }
             }
         }
@@ -479,18 +530,17 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
                 for (int i = 0; i < 4; ++i) sums[((h * NT + n) * 4 + i) * 32 + lane] = tot[h][n][i];
         // the next round's first weights are on their way before this one is
         // added up, and its rows while it is
-        W4Round next = cur;
-        const bool more = cur.left > 0;
-        const int cur_slot = slot, part = warp & ((1 << cur.log_ks) - 1);
+        const bool other_rows = more && next.group != cur.group;
         if (more) {
-            w4_next_round<kWarps>(next, sp, args.tiles, args.nseg, base, most);
-            first_blocks(next);
+            mine = then;
+#pragma unroll
+            for (int i = 0; i < kStages; ++i) load(st[i], mine, i);
         }
-        const bool other_rows = next.seg != cur.seg || next.chunk != cur.chunk;
         // (two buffers of sums in turn: the barrier of the next round lies between
         // this round's reads and the writes of the round after)
         __syncthreads();
-        if (more && other_rows) fetch_rows(next);
+        if (other_rows) fetch_rows(next);
+        const int cur_slot = warp >> cur.log_ks, part = warp & ((1 << cur.log_ks) - 1);
         if (cur_slot < cur.tiles) {
             // lane 4r + c, value i: row r + 8 (i / 2) of half h, column 8n + 2c + i % 2
             const int ks = 1 << cur.log_ks, tile = cur.tile + cur_slot;
@@ -499,13 +549,13 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
             for (int v = part * 32 + lane; v < kOut; v += ks * 32) {
                 const int i = (v >> 5) & 3, n = (v >> 7) % NT, h = v / (kVals / 2);
                 const int col = 8 * n + 2 * c + (i & 1);
-                if (col >= nrows) continue;
+                if (col >= cur.nrows) continue;
                 float g = 0.0f, u = 0.0f;
                 for (int w = 0; w < ks; ++w) {
                     g += from[w][v];
                     if constexpr (!DOWN) u += from[w][v + kVals / 2];
                 }
-                const int64_t row = sp.out_row0[cur.seg] + row0 + col;
+                const int64_t row = sp.out_row0[cur.seg] + cur.row0 + col;
                 if (i >= 2) {  // row r + 8 carries 16 u
                     g *= 0.0625f;
                     u *= 0.0625f;
