@@ -18,7 +18,10 @@
 namespace moe {
 
 constexpr int kNormMaxH = 16384;
-constexpr int kNormVec = 4;  // 16-byte vectors of a row per thread
+
+// Most threads of a CTA whose threads hold VPT vectors of a row.
+template <typename T, int VPT>
+constexpr int kNormThreads = VPT == 2 || sizeof(T) == 2 ? 512 : 1024;
 
 // The 16-byte vector of values f rounded to the row type.
 template <typename T>
@@ -36,8 +39,8 @@ __device__ __forceinline__ uint4 pack_vec(const float (&f)[16 / sizeof(T)]) {
 }
 
 // Sum of a and of b over the threads of one row: a warp, or the whole CTA of
-// blockDim.x threads (kWarp false; s_red holds 2 * 32 floats, and the caller
-// leaves a barrier between two uses of it).  With kMaxB b takes the maximum.
+// blockDim.x threads (kWarp false; s_red holds 2 * 32 floats, and a barrier lies
+// between two uses of it).  With kMaxB b takes the maximum.
 // Every thread gets both results, added in one fixed order.
 template <bool kWarp, bool kMaxB>
 __device__ __forceinline__ void row_reduce(float& a, float& b, float* s_red) {
@@ -65,56 +68,39 @@ __device__ __forceinline__ void row_reduce(float& a, float& b, float* s_red) {
     }
 }
 
-// One row per warp (kWarp: blockDim.x / 32 rows per CTA) or per CTA.  A row
-// stays in registers between its only read and its only write, so outputs may
-// overlay the inputs of the same rows.  Both statistics come from one
+// Asynchronous copy of one 16-byte vector of a row into the thread's own bytes
+// of the ring, and the wait for all but the newest N rows of copies.
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ring_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A row in registers -> residual_out, y, codes.  Both statistics come from one
 // reduction: y = (s * w) * r is monotone in s * w for the row's r >= 0, so the
 // largest |y| is the rounded product of the largest |s * w| with r.
-template <typename T, bool kWarp>
-__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(
-    const T* x, const T* res, const T* __restrict__ weight, float eps, int64_t n_rows, int H,
-    T* res_out, T* y, uint8_t* y_q, float* __restrict__ y_scale) {
+template <typename T, bool kWarp, int VPT>
+__device__ __forceinline__ void norm_row(const uint4 (&xv)[VPT], const uint4 (&rv)[VPT],
+                                         const uint4 (&wv)[VPT], bool has_res, float eps, int H,
+                                         int tx, int nt, T* res_out, T* y, uint8_t* y_q,
+                                         float* y_scale, float* s_red) {
     constexpr int kVE = 16 / static_cast<int>(sizeof(T));
-    __shared__ float s_red[64];
-    const int tx = kWarp ? (threadIdx.x & 31) : threadIdx.x;
-    const int nt = kWarp ? 32 : blockDim.x;
-    const int64_t row = kWarp ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) +
-                                    (threadIdx.x >> 5)
-                              : static_cast<int64_t>(blockIdx.x);
-    if (kWarp && row >= n_rows) return;
     const int nv = H / kVE;
-    ptx::grid_dep_wait();
-    const uint4* xr = reinterpret_cast<const uint4*>(x + row * H);
-    const uint4* rr = reinterpret_cast<const uint4*>(res ? res + row * H : nullptr);
-    const uint4* wr = reinterpret_cast<const uint4*>(weight);
-    uint4 xv[kNormVec], rv[kNormVec], wv[kNormVec];
-#pragma unroll
-    for (int u = 0; u < kNormVec; ++u) {
-        const int v = tx + u * nt;
-        xv[u] = rv[u] = wv[u] = make_uint4(0, 0, 0, 0);
-        if (v < nv) {
-            xv[u] = xr[v];
-            if (res) rv[u] = rr[v];
-            wv[u] = wr[v];
-        }
-    }
-    float s[kNormVec][kVE];
+    float s[VPT][kVE];
     float sq = 0.0f, big = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kNormVec; ++u) {
+    for (int u = 0; u < VPT; ++u) {
         unpack_vec<T>(xv[u], s[u]);
         float w[kVE];
         unpack_vec<T>(wv[u], w);
-        if (res) {
+        if (has_res) {
             float b[kVE];
             unpack_vec<T>(rv[u], b);
 #pragma unroll
             for (int e = 0; e < kVE; ++e) s[u][e] += b[e];
-            if (res_out && tx + u * nt < nv)
-                reinterpret_cast<uint4*>(res_out + row * H)[tx + u * nt] = pack_vec<T>(s[u]);
-        } else if (res_out && tx + u * nt < nv) {
-            reinterpret_cast<uint4*>(res_out + row * H)[tx + u * nt] = xv[u];
         }
+        if (res_out && tx + u * nt < nv)
+            reinterpret_cast<uint4*>(res_out)[tx + u * nt] = pack_vec<T>(s[u]);
 #pragma unroll
         for (int e = 0; e < kVE; ++e) {
             sq = fmaf(s[u][e], s[u][e], sq);
@@ -130,16 +116,16 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(
         if constexpr (sizeof(T) == 2) amax = __bfloat162float(__float2bfloat16_rn(amax));
         const float sc = pow2_scale_f(amax);
         inv = 1.0f / sc;  // exact: power of two
-        if (tx == 0) y_scale[row] = sc;
+        if (tx == 0) *y_scale = sc;
     }
 #pragma unroll
-    for (int u = 0; u < kNormVec; ++u) {
+    for (int u = 0; u < VPT; ++u) {
         const int v = tx + u * nt;
         if (v >= nv) continue;
 #pragma unroll
         for (int e = 0; e < kVE; ++e) s[u][e] *= r;
         const uint4 q = pack_vec<T>(s[u]);
-        if (y) reinterpret_cast<uint4*>(y + row * H)[v] = q;
+        if (y) reinterpret_cast<uint4*>(y)[v] = q;
         if (y_q) {
             // the codes are those of the stored (rounded) row, so they equal
             // the ones the FP8 forward makes itself of y
@@ -152,51 +138,169 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(
                        (static_cast<uint32_t>(
                             ptx::e4m3x2(f[4 * k + 2] * inv, f[4 * k + 3] * inv))
                         << 16);
-            if constexpr (kVE == 8)
-                reinterpret_cast<uint2*>(y_q + row * H)[v] = make_uint2(c[0], c[1]);
-            else
-                reinterpret_cast<uint32_t*>(y_q + row * H)[v] = c[0];
+            if constexpr (kVE == 8) reinterpret_cast<uint2*>(y_q)[v] = make_uint2(c[0], c[1]);
+            else reinterpret_cast<uint32_t*>(y_q)[v] = c[0];
         }
     }
 }
 
-// Backward over rows blockIdx.x, blockIdx.x + gridDim.x, ...: dx of each row,
-// and the CTA's share of dw, kept in registers and written once to
-// partial[blockIdx.x].  Thread tx owns the same columns of every row.
-template <typename T>
-__global__ void __launch_bounds__(1024) add_rmsnorm_backward_kernel(
-    const T* dy, const T* dres, const T* h, const T* __restrict__ weight, float eps,
-    int64_t n_rows, int H, T* dx, float* __restrict__ partial) {
+// Short rows: one per warp, four per CTA, VPT vectors per lane.
+template <typename T, int VPT>
+__global__ void __launch_bounds__(128) add_rmsnorm_short_kernel(
+    const T* x, const T* res, const T* __restrict__ weight, float eps, int64_t n_rows, int H,
+    T* res_out, T* y, uint8_t* y_q, float* __restrict__ y_scale) {
     constexpr int kVE = 16 / static_cast<int>(sizeof(T));
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    if (row >= n_rows) return;
+    const int nv = H / kVE;
+    ptx::grid_dep_wait();
+    uint4 xv[VPT], rv[VPT], wv[VPT];
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+        const int v = lane + u * 32;
+        xv[u] = rv[u] = wv[u] = make_uint4(0, 0, 0, 0);
+        if (v < nv) {
+            xv[u] = reinterpret_cast<const uint4*>(x + row * H)[v];
+            if (res) rv[u] = reinterpret_cast<const uint4*>(res + row * H)[v];
+            wv[u] = reinterpret_cast<const uint4*>(weight)[v];
+        }
+    }
+    norm_row<T, true, VPT>(xv, rv, wv, res != nullptr, eps, H, lane, 32,
+                           res_out ? res_out + row * H : nullptr, y ? y + row * H : nullptr,
+                           y_q ? y_q + row * H : nullptr, y_q ? y_scale + row : nullptr, nullptr);
+}
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ..., one at a time per CTA, VPT
+// vectors per thread.  The inputs of the next D - 1 rows are on their way into a
+// ring in shared memory; each thread copies and reads its own columns only, so
+// the ring needs no barrier, and an output may overlay the inputs of the same
+// row.  (One row per CTA without the ring left the loads' latency in the open:
+// 65 us against 41 for 4096 rows of 6144 bf16 with residual and codes.)
+template <typename T, int VPT, int D>
+__global__ void __launch_bounds__(kNormThreads<T, VPT>) add_rmsnorm_kernel(
+    const T* x, const T* res, const T* __restrict__ weight, float eps, int64_t n_rows, int H,
+    T* res_out, T* y, uint8_t* y_q, float* __restrict__ y_scale) {
+    constexpr int kVE = 16 / static_cast<int>(sizeof(T));
+    extern __shared__ __align__(16) uint8_t s_ring[];
     __shared__ float s_red[2][64];
     const int tx = threadIdx.x, nt = blockDim.x;
     const int nv = H / kVE;
+    uint4* ring = reinterpret_cast<uint4*>(s_ring);  // [D][x, res][nv]
+    const int per_stage = (res ? 2 : 1) * nv;
     ptx::grid_dep_wait();
-    uint4 wv[kNormVec];
-    float dw[kNormVec][kVE];
+    auto fill = [&](int64_t row, int stage) {
+        if (row < n_rows) {
 #pragma unroll
-    for (int u = 0; u < kNormVec; ++u) {
+            for (int u = 0; u < VPT; ++u) {
+                const int v = tx + u * nt;
+                if (v < nv) {
+                    uint4* dst = ring + stage * per_stage + v;
+                    ptx::cp_async_16(dst, reinterpret_cast<const uint4*>(x + row * H) + v, 16);
+                    if (res)
+                        ptx::cp_async_16(dst + nv,
+                                         reinterpret_cast<const uint4*>(res + row * H) + v, 16);
+                }
+            }
+        }
+        ring_commit();
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) fill(blockIdx.x + static_cast<int64_t>(d) * gridDim.x, d);
+    uint4 wv[VPT];
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+        const int v = tx + u * nt;
+        wv[u] = v < nv ? reinterpret_cast<const uint4*>(weight)[v] : make_uint4(0, 0, 0, 0);
+    }
+    int stage = 0, flip = 0;
+    for (int64_t row = blockIdx.x; row < n_rows; row += gridDim.x, flip ^= 1) {
+        ring_wait<D - 1>();
+        uint4 xv[VPT], rv[VPT];
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const int v = tx + u * nt;
+            xv[u] = rv[u] = make_uint4(0, 0, 0, 0);
+            if (v < nv) {
+                xv[u] = ring[stage * per_stage + v];
+                if (res) rv[u] = ring[stage * per_stage + nv + v];
+            }
+        }
+        fill(row + static_cast<int64_t>(D) * gridDim.x, stage);
+        if (++stage == D) stage = 0;
+        // two scratch rows in turn: the barrier inside the next row's reduction
+        // separates this row's reads from the writes two rows later
+        norm_row<T, false, VPT>(xv, rv, wv, res != nullptr, eps, H, tx, nt,
+                                res_out ? res_out + row * H : nullptr, y ? y + row * H : nullptr,
+                                y_q ? y_q + row * H : nullptr, y_q ? y_scale + row : nullptr,
+                                s_red[flip]);
+    }
+}
+
+// Backward over rows blockIdx.x, blockIdx.x + gridDim.x, ..., with the same ring:
+// dx of each row, and the CTA's share of dw, kept in registers (a thread owns the
+// same columns of every row) and written once to partial[blockIdx.x].
+template <typename T, int VPT, int D>
+__global__ void __launch_bounds__(kNormThreads<T, VPT>) add_rmsnorm_backward_kernel(
+    const T* dy, const T* dres, const T* h, const T* __restrict__ weight, float eps,
+    int64_t n_rows, int H, T* dx, float* __restrict__ partial) {
+    constexpr int kVE = 16 / static_cast<int>(sizeof(T));
+    extern __shared__ __align__(16) uint8_t s_ring[];
+    __shared__ float s_red[2][64];
+    const int tx = threadIdx.x, nt = blockDim.x;
+    const int nv = H / kVE;
+    uint4* ring = reinterpret_cast<uint4*>(s_ring);  // [D][h, dy, dres][nv]
+    const int per_stage = (dres ? 3 : 2) * nv;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    auto fill = [&](int64_t row, int stage) {
+        if (row < n_rows) {
+#pragma unroll
+            for (int u = 0; u < VPT; ++u) {
+                const int v = tx + u * nt;
+                if (v < nv) {
+                    uint4* dst = ring + stage * per_stage + v;
+                    ptx::cp_async_16(dst, reinterpret_cast<const uint4*>(h + row * H) + v, 16);
+                    ptx::cp_async_16(dst + nv, reinterpret_cast<const uint4*>(dy + row * H) + v,
+                                     16);
+                    if (dres)
+                        ptx::cp_async_16(dst + 2 * nv,
+                                         reinterpret_cast<const uint4*>(dres + row * H) + v, 16);
+                }
+            }
+        }
+        ring_commit();
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) fill(blockIdx.x + static_cast<int64_t>(d) * gridDim.x, d);
+    uint4 wv[VPT];
+    float dw[VPT][kVE];
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
         const int v = tx + u * nt;
         wv[u] = v < nv ? reinterpret_cast<const uint4*>(weight)[v] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int e = 0; e < kVE; ++e) dw[u][e] = 0.0f;
     }
-    int flip = 0;
+    int stage = 0, flip = 0;
     for (int64_t row = blockIdx.x; row < n_rows; row += gridDim.x, flip ^= 1) {
-        uint4 hv[kNormVec], gv[kNormVec], rv[kNormVec];
+        ring_wait<D - 1>();
+        uint4 hv[VPT], gv[VPT], rv[VPT];
 #pragma unroll
-        for (int u = 0; u < kNormVec; ++u) {
+        for (int u = 0; u < VPT; ++u) {
             const int v = tx + u * nt;
             hv[u] = gv[u] = rv[u] = make_uint4(0, 0, 0, 0);
             if (v < nv) {
-                hv[u] = reinterpret_cast<const uint4*>(h + row * H)[v];
-                gv[u] = reinterpret_cast<const uint4*>(dy + row * H)[v];
-                if (dres) rv[u] = reinterpret_cast<const uint4*>(dres + row * H)[v];
+                hv[u] = ring[stage * per_stage + v];
+                gv[u] = ring[stage * per_stage + nv + v];
+                if (dres) rv[u] = ring[stage * per_stage + 2 * nv + v];
             }
         }
+        fill(row + static_cast<int64_t>(D) * gridDim.x, stage);
+        if (++stage == D) stage = 0;
         float sq = 0.0f, dot = 0.0f;
 #pragma unroll
-        for (int u = 0; u < kNormVec; ++u) {
+        for (int u = 0; u < VPT; ++u) {
             float hf[kVE], gf[kVE], wf[kVE];
             unpack_vec<T>(hv[u], hf);
             unpack_vec<T>(gv[u], gf);
@@ -207,13 +311,11 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_backward_kernel(
                 dot = fmaf(gf[e] * wf[e], hf[e], dot);
             }
         }
-        // two scratch rows in turn: the barrier inside the next row's reduction
-        // separates this row's reads from the writes two rows later
         row_reduce<false, false>(sq, dot, s_red[flip]);
         const float r = 1.0f / sqrtf(sq / static_cast<float>(H) + eps);
         const float c = r * r * (dot / static_cast<float>(H));  // mean(g * n) * r
 #pragma unroll
-        for (int u = 0; u < kNormVec; ++u) {
+        for (int u = 0; u < VPT; ++u) {
             const int v = tx + u * nt;
             float hf[kVE], gf[kVE], wf[kVE], rf[kVE];
             unpack_vec<T>(hv[u], hf);
@@ -229,7 +331,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_backward_kernel(
         }
     }
 #pragma unroll
-    for (int u = 0; u < kNormVec; ++u) {
+    for (int u = 0; u < VPT; ++u) {
         const int v = tx + u * nt;
         if (v < nv) {
             float4* p = reinterpret_cast<float4*>(partial + static_cast<int64_t>(blockIdx.x) * H) +
@@ -241,24 +343,24 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_backward_kernel(
     }
 }
 
-// dw[c] = sum of partial[0..n)[c] in a fixed order: 8 warps take every 8th row
+// dw[c] = sum of partial[0..n)[c] in a fixed order: 32 warps take every 32nd row
 // of 32 columns, then their sums are added in warp order.
-__global__ void __launch_bounds__(256) reduce_columns_kernel(const float* __restrict__ partial,
-                                                             int n, int H,
-                                                             float* __restrict__ dw) {
-    __shared__ float s_sum[8][32];
+__global__ void __launch_bounds__(1024) reduce_columns_kernel(const float* __restrict__ partial,
+                                                              int n, int H,
+                                                              float* __restrict__ dw) {
+    __shared__ float s_sum[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;  // H is a multiple of 64
     ptx::grid_dep_wait();
     float a = 0.0f;
-#pragma unroll 8
-    for (int i = warp; i < n; i += 8) a += partial[static_cast<int64_t>(i) * H + c];
+#pragma unroll 4
+    for (int i = warp; i < n; i += 32) a += partial[static_cast<int64_t>(i) * H + c];
     s_sum[warp][lane] = a;
     __syncthreads();
     if (warp == 0) {
         a = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) a += s_sum[w][lane];
+        for (int w = 0; w < 32; ++w) a += s_sum[w][lane];
         dw[c] = a;
     }
 }

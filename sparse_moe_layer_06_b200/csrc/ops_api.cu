@@ -24,55 +24,141 @@ int32_t check_norm(const moe_problem* p, float eps) {
     return MOE_OK;
 }
 
-// Threads of one row: kNormVec vectors each, whole warps.
-int norm_threads(const moe_problem* p) {
-    const int nv = p->H * (p->dtype == MOE_BF16 ? 2 : 4) / 16;
-    return std::max(32, ((nv + kNormVec - 1) / kNormVec + 31) / 32 * 32);
+// How a launch over rows of H values covers them: VPT 16-byte vectors per
+// thread (2 up to 1024 vectors, 4 above), CTAs per SM (about `per_sm` threads),
+// and the depth of their rings.
+struct RowShape {
+    int nv, vpt, threads, ctas, depth, smem;
+};
+
+constexpr int kNormThreadsPerSM = 768, kNormBackThreadsPerSM = 512;
+constexpr int kRingBytesPerSM = 200 * 1024;
+
+RowShape row_shape(const moe_problem* p, int inputs, int per_sm) {
+    RowShape r;
+    const int row_bytes = p->H * (p->dtype == MOE_BF16 ? 2 : 4);
+    r.nv = row_bytes / 16;
+    r.vpt = r.nv <= 1024 ? 2 : 4;
+    r.threads = std::max(32, ((r.nv + r.vpt - 1) / r.vpt + 31) / 32 * 32);
+    r.ctas = std::max(1, std::min(8, per_sm / r.threads));
+    const int rows = kRingBytesPerSM / r.ctas / (inputs * row_bytes);
+    r.depth = rows >= 4 ? 4 : (rows >= 2 ? 2 : 1);
+    r.smem = r.depth * inputs * row_bytes;
+    return r;
+}
+
+// Lets `kern` take the ring's shared memory, once per device.
+template <typename K>
+bool allow_ring(K kern, std::atomic<uint64_t>& configured) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit && (configured.load() & bit)) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kRingBytesPerSM) != cudaSuccess)
+        return false;
+    configured.fetch_or(bit);
+    return true;
+}
+
+template <typename T, int VPT, int D>
+int32_t launch_norm(const moe_problem* p, const RowShape& r, const void* x, const void* res,
+                    const void* weight, float eps, void* res_out, void* y, uint8_t* y_q,
+                    float* y_scale, cudaStream_t s) {
+    auto kern = add_rmsnorm_kernel<T, VPT, D>;
+    static std::atomic<uint64_t> configured{0};
+    if (!allow_ring(kern, configured)) return MOE_ERR_CUDA;
+    const int64_t most = static_cast<int64_t>(sm_count()) * r.ctas;
+    MOE_LAUNCH("add_rmsnorm", s,
+               if (launch_ex(kern, static_cast<int>(std::min<int64_t>(p->T, most)), r.threads,
+                             r.smem, s, pdl_enabled(), static_cast<const T*>(x),
+                             static_cast<const T*>(res), static_cast<const T*>(weight), eps, p->T,
+                             p->H, static_cast<T*>(res_out), static_cast<T*>(y), y_q, y_scale) !=
+                   cudaSuccess) return MOE_ERR_CUDA);
+    return MOE_OK;
+}
+
+template <typename T, int VPT>
+int32_t launch_norm_short(const moe_problem* p, const void* x, const void* res,
+                          const void* weight, float eps, void* res_out, void* y, uint8_t* y_q,
+                          float* y_scale, cudaStream_t s) {
+    MOE_LAUNCH("add_rmsnorm_short", s,
+               if (launch_ex(add_rmsnorm_short_kernel<T, VPT>, static_cast<int>((p->T + 3) / 4),
+                             128, 0, s, pdl_enabled(), static_cast<const T*>(x),
+                             static_cast<const T*>(res), static_cast<const T*>(weight), eps, p->T,
+                             p->H, static_cast<T*>(res_out), static_cast<T*>(y), y_q, y_scale) !=
+                   cudaSuccess) return MOE_ERR_CUDA);
+    return MOE_OK;
 }
 
 template <typename T>
 int32_t run_norm(const moe_problem* p, const void* x, const void* res, const void* weight,
                  float eps, void* res_out, void* y, uint8_t* y_q, float* y_scale,
                  cudaStream_t s) {
-    const int nt = norm_threads(p);
-    const bool warp = nt == 32;
-    const int threads = warp ? 128 : nt;
-    const int64_t rows = warp ? (p->T + 3) / 4 : p->T;
-    auto kern = warp ? add_rmsnorm_kernel<T, true> : add_rmsnorm_kernel<T, false>;
-    MOE_LAUNCH("add_rmsnorm", s,
-               if (launch_ex(kern, static_cast<int>(rows), threads, 0, s, pdl_enabled(),
-                             static_cast<const T*>(x), static_cast<const T*>(res),
-                             static_cast<const T*>(weight), eps, p->T, p->H,
-                             static_cast<T*>(res_out), static_cast<T*>(y), y_q, y_scale) !=
-                   cudaSuccess) return MOE_ERR_CUDA);
-    return MOE_OK;
+    const RowShape r = row_shape(p, res ? 2 : 1, kNormThreadsPerSM);
+    if (r.nv <= 64)
+        return launch_norm_short<T, 2>(p, x, res, weight, eps, res_out, y, y_q, y_scale, s);
+    if (r.nv <= 128)
+        return launch_norm_short<T, 4>(p, x, res, weight, eps, res_out, y, y_q, y_scale, s);
+#define MOE_NORM(V, D) \
+    return launch_norm<T, V, D>(p, r, x, res, weight, eps, res_out, y, y_q, y_scale, s)
+    if (r.vpt == 2) {
+        if (r.depth == 4) MOE_NORM(2, 4);
+        MOE_NORM(2, 2);
+    }
+    if (r.depth == 4) MOE_NORM(4, 4);
+    if (r.depth == 2) MOE_NORM(4, 2);
+    MOE_NORM(4, 1);
+#undef MOE_NORM
 }
 
-// CTAs of the backward pass: as many rows for each, and about kNormBackCtas
-// CTAs (the workspace holds a partial dw of each).
-constexpr int64_t kNormBackCtas = 148 * 3;
-int64_t norm_backward_ctas(int64_t T) {
-    if (T <= 0) return 1;
-    const int64_t per = (T + kNormBackCtas - 1) / kNormBackCtas;
-    return (T + per - 1) / per;
+// CTAs of the backward pass, as many rows for each (the workspace holds a
+// partial dw of each CTA; the count goes by 148 SMs on any device, so that it
+// depends on the problem only).
+constexpr int64_t kNormBackSMs = 148;
+int64_t norm_backward_ctas(const moe_problem* p) {
+    if (p->T <= 0) return 1;
+    const int64_t most = kNormBackSMs * row_shape(p, 3, kNormBackThreadsPerSM).ctas;
+    const int64_t per = (p->T + most - 1) / most;
+    return (p->T + per - 1) / per;
+}
+
+template <typename T, int VPT, int D>
+int32_t launch_norm_backward(const moe_problem* p, const RowShape& r, const void* dy,
+                             const void* dres, const void* h, const void* weight, float eps,
+                             void* dx, float* dweight, float* partial, cudaStream_t s) {
+    auto kern = add_rmsnorm_backward_kernel<T, VPT, D>;
+    static std::atomic<uint64_t> configured{0};
+    if (!allow_ring(kern, configured)) return MOE_ERR_CUDA;
+    const int ctas = static_cast<int>(norm_backward_ctas(p));
+    MOE_LAUNCH("add_rmsnorm_backward", s,
+               if (launch_ex(kern, ctas, r.threads, r.smem, s, pdl_enabled(),
+                             static_cast<const T*>(dy), static_cast<const T*>(dres),
+                             static_cast<const T*>(h), static_cast<const T*>(weight), eps, p->T,
+                             p->H, static_cast<T*>(dx), partial) != cudaSuccess)
+                   return MOE_ERR_CUDA);
+    MOE_LAUNCH("add_rmsnorm_dweight", s,
+               if (launch_ex(reduce_columns_kernel, p->H / 32, 1024, 0, s, pdl_enabled(),
+                             static_cast<const float*>(partial), ctas, p->H, dweight) !=
+                   cudaSuccess) return MOE_ERR_CUDA);
+    return MOE_OK;
 }
 
 template <typename T>
 int32_t run_norm_backward(const moe_problem* p, const void* dy, const void* dres, const void* h,
                           const void* weight, float eps, void* dx, float* dweight,
                           float* partial, cudaStream_t s) {
-    const int ctas = static_cast<int>(norm_backward_ctas(p->T));
-    MOE_LAUNCH("add_rmsnorm_backward", s,
-               if (launch_ex(add_rmsnorm_backward_kernel<T>, ctas, norm_threads(p), 0, s,
-                             pdl_enabled(), static_cast<const T*>(dy),
-                             static_cast<const T*>(dres), static_cast<const T*>(h),
-                             static_cast<const T*>(weight), eps, p->T, p->H,
-                             static_cast<T*>(dx), partial) != cudaSuccess) return MOE_ERR_CUDA);
-    MOE_LAUNCH("add_rmsnorm_dweight", s,
-               if (launch_ex(reduce_columns_kernel, p->H / 32, 256, 0, s, pdl_enabled(),
-                             static_cast<const float*>(partial), ctas, p->H, dweight) !=
-                   cudaSuccess) return MOE_ERR_CUDA);
-    return MOE_OK;
+    const RowShape r = row_shape(p, dres ? 3 : 2, kNormBackThreadsPerSM);
+#define MOE_NORM(V, D) \
+    return launch_norm_backward<T, V, D>(p, r, dy, dres, h, weight, eps, dx, dweight, partial, s)
+    if (r.vpt == 2) {
+        if (r.depth == 4) MOE_NORM(2, 4);
+        MOE_NORM(2, 2);
+    }
+    if (r.depth == 4) MOE_NORM(4, 4);
+    if (r.depth == 2) MOE_NORM(4, 2);
+    MOE_NORM(4, 1);
+#undef MOE_NORM
 }
 
 // ------------------------------------------------------------------ balance loss
@@ -311,7 +397,7 @@ size_t operator_workspace(const moe_problem* p, int32_t call) {
     switch (call) {
         case MOE_CALL_ADD_RMSNORM_BACKWARD:
             if (p->H > kNormMaxH) return 0;
-            return 256 + static_cast<size_t>(norm_backward_ctas(p->T)) * p->H * 4;
+            return 256 + static_cast<size_t>(norm_backward_ctas(p)) * p->H * 4;
         case MOE_CALL_BALANCE_LOSS: return balance_layout(p, 1).total;
         case MOE_CALL_EXPERTS_W4:
         case MOE_CALL_FORWARD_W4:

@@ -60,9 +60,9 @@ def norm_dx_bound(dx, mag, dtype):
 
 
 def norm_dw_bound(mag, T):
-    # r (28), two products; a CTA's rows (at most T/444 + 1), 56 partials per
-    # warp, 8 warps
-    return mag * (28 + 2 + T / 444 + 1 + 56 + 8) * 2.0 ** -24
+    # r (28), two products; a CTA's rows (at most T/148 + 1), 37 partials (of at
+    # most 1184) per warp, 32 warps
+    return mag * (28 + 2 + T / 148 + 1 + 37 + 32) * 2.0 ** -24
 
 
 # ------------------------------------------------------------------ balance loss
