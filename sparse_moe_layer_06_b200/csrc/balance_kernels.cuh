@@ -19,61 +19,112 @@
 
 namespace moe {
 
-constexpr int kBalPer = kMaxExperts / 32;  // experts per lane
+// A token's E logits lie in one warp, NP per lane: expert lane + 32 i in slot i,
+// or, with VEC, expert 128 (i / 4) + 4 lane + i % 4 (E a multiple of 4, rows 16
+// byte aligned), so that a lane loads four at a time.
+template <bool VEC>
+__device__ __forceinline__ int slot_expert(int i) {
+    const int lane = threadIdx.x & 31;
+    return VEC ? 128 * (i >> 2) + 4 * lane + (i & 3) : lane + 32 * i;
+}
 
-// First sequence that ends behind token t (n_seq if none).  Offsets that are
-// not in order give some sequence number, never one out of range.
+// v[i] = row[expert of slot i], `fill` beyond the E experts.
+template <int NP, bool VEC>
+__device__ __forceinline__ void load_slots(const float* __restrict__ row, int E, float fill,
+                                           float (&v)[NP]) {
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < NP; i += 4) {
+            const int e = slot_expert<VEC>(i);
+            float4 q = make_float4(fill, fill, fill, fill);
+            if (e < E) q = *reinterpret_cast<const float4*>(row + e);
+            v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int e = slot_expert<VEC>(i);
+            v[i] = e < E ? row[e] : fill;
+        }
+    }
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+
+// First sequence that ends behind token t (n_seq if none), by one warp: 32 places
+// of the range are looked at in each round, so up to 1024 sequences take two
+// loads, one behind the other.  Offsets that are not in order give some sequence
+// number, never one out of range.
 __device__ __forceinline__ int first_sequence(const int32_t* __restrict__ offsets, int n_seq,
                                               int64_t t) {
-    int lo = 0, hi = n_seq;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (offsets[mid + 1] > t) hi = mid;
-        else lo = mid + 1;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = n_seq;
+    while (len > 0) {
+        const int step = (len + 31) / 32;
+        // sequence lo + (lane + 1) step - 1 and all before it end at t or earlier?
+        const int at = (lane + 1) * step - 1;
+        const bool before = at < len && offsets[lo + at + 1] <= t;
+        const int n = __popc(__ballot_sync(0xffffffffu, before));
+        lo += n * step;
+        len = step == 1 ? 0 : min(step - 1, len - n * step);
     }
-    return lo;
+    return min(lo, n_seq);
 }
 
-// Softmax of one token's E logits by one warp, lane + 32 i holding expert
-// lane + 32 i.  A token whose logits are all -inf (every expert masked off)
-// has no distribution: its probabilities are 0.
-__device__ __forceinline__ void token_probs(const float* __restrict__ row,
-                                            const float* __restrict__ bias, int E,
-                                            float (&p)[kBalPer]) {
+// Bits of the tokens t .. t + 31 that lie before `end` and have their mask set.
+__device__ __forceinline__ uint32_t live_tokens(const uint8_t* __restrict__ mask, int64_t t,
+                                                int64_t end) {
     const int lane = threadIdx.x & 31;
-    float mx = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kBalPer; ++i) {
-        const int e = lane + 32 * i;
-        p[i] = e < E ? row[e] : -INFINITY;
-    }
-#pragma unroll
-    for (int i = 0; i < kBalPer; ++i) {
-        const int e = lane + 32 * i;
-        if (bias && e < E) p[i] += bias[e];
-        mx = fmaxf(mx, p[i]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (mx == -INFINITY) mx = 0.0f;  // (a NaN logit still gives NaN below)
-    float z = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kBalPer; ++i) {
-        p[i] = expf(p[i] - mx);
-        z += p[i];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-#pragma unroll
-    for (int i = 0; i < kBalPer; ++i) p[i] *= inv;
+    return __ballot_sync(0xffffffffu, t + lane < end && (!mask || mask[t + lane]));
 }
+
+// Tokens whose logits a warp has on the way at once: 4 KB of 256 experts, which
+// at 24 warps per SM covers the memory's latency (one token ahead did not: 34 us
+// against 26 for the gradient of 65536 x 256 logits).
+constexpr int kBalBatch = 4;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Numerators of the softmax of one token's logits l plus the bias (read again
+// for each token: registers hold the logits on the way instead).  A token whose
+// logits are all -inf (every expert masked off) has no distribution: its
+// probabilities are 0.
+template <int NP, bool VEC>
+__device__ __forceinline__ void numerators(const float* __restrict__ bias, int E, float (&l)[NP]) {
+    if (bias) {
+        float b[NP];
+        load_slots<NP, VEC>(bias, E, 0.0f, b);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) l[i] += b[i];
+    }
+    float mx = l[0];
+#pragma unroll
+    for (int i = 1; i < NP; ++i) mx = fmaxf(mx, l[i]);
+    mx = warp_max(mx);
+    if (mx == -INFINITY) mx = 0.0f;  // (a NaN logit still gives NaN below)
+    // (the difference first: the products of the lowest floats are infinite)
+    constexpr float kLog2e = 1.44269504f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) l[i] = exp2_approx((l[i] - mx) * kLog2e);
+}
+
+// Floats from one slot of partial sums to the next: whole 16-byte vectors.
+__host__ __device__ constexpr int balance_pad(int E) { return (E + 3) & ~3; }
 
 // Pass 1: CTA b sums the probabilities and counts of the tokens of window b
 // ([b * win, (b+1) * win)) for each sequence s that the window touches, into
 // slot b + s: along the windows and sequences in order either b or s grows by
 // one, so no two pairs share a slot.
-__global__ void __launch_bounds__(256) balance_partial_kernel(
+template <int NP, bool VEC>
+__global__ void __launch_bounds__(256, 3) balance_partial_kernel(
     const float* __restrict__ logits, const float* __restrict__ bias,
     const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask,
     const int32_t* __restrict__ offsets, int n_seq, int64_t T, int E, int k, int win,
@@ -84,6 +135,7 @@ __global__ void __launch_bounds__(256) balance_partial_kernel(
     __shared__ int32_t s_tok;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
     if (blockIdx.x == 0 && tid == 0) *ticket = 0;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * win;
     const int64_t t1 = min(T, t0 + win);
@@ -96,34 +148,60 @@ __global__ void __launch_bounds__(256) balance_partial_kernel(
         s_cnt[tid] = 0;
         if (tid == 0) s_tok = 0;
         __syncthreads();
-        float acc[kBalPer];
+        float acc[NP];
 #pragma unroll
-        for (int i = 0; i < kBalPer; ++i) acc[i] = 0.0f;
+        for (int i = 0; i < NP; ++i) acc[i] = 0.0f;
         int ntok = 0;
-        for (int64_t t = lo + warp; t < hi; t += 8) {
-            if (mask && !mask[t]) continue;
-            ++ntok;
-            if (lane < k) {
-                const int e = idx[t * k + lane];
-                if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
-                else set_device_error(status, DEV_ERR_BAD_INDEX);
-            }
-            float p[kBalPer];
-            token_probs(logits + t * E, bias, E, p);
+        // each warp takes an eighth of the window
+        const int64_t end = min(hi, t0 + static_cast<int64_t>(warp + 1) * (win / 8));
+        const int64_t first = max(lo, t0 + static_cast<int64_t>(warp) * (win / 8));
+        uint32_t bits = 0;
+        for (int64_t t = first; t < end; t += kBalBatch) {
+            if (((t - first) & 31) == 0) bits = live_tokens(mask, t, end);
+            const uint32_t live = bits >> ((t - first) & 31);
+            float l[kBalBatch][NP];
+            int e[kBalBatch];
 #pragma unroll
-            for (int i = 0; i < kBalPer; ++i) acc[i] += p[i];
+            for (int u = 0; u < kBalBatch; ++u) {
+                if (live >> u & 1) {
+                    e[u] = lane < k ? idx[(t + u) * k + lane] : 0;
+                    load_slots<NP, VEC>(logits + (t + u) * E, E, -INFINITY, l[u]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kBalBatch; ++u) {
+                if (!(live >> u & 1)) continue;
+                ++ntok;
+                if (lane < k) {
+                    if (e[u] >= 0 && e[u] < E) atomicAdd(&s_cnt[e[u]], 1);
+                    else set_device_error(status, DEV_ERR_BAD_INDEX);
+                }
+                numerators<NP, VEC>(bias, E, l[u]);
+                float z = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NP; ++i) z += l[u][i];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+                const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+#pragma unroll
+                for (int i = 0; i < NP; ++i) acc[i] = fmaf(l[u][i], inv, acc[i]);
+            }
         }
         if (lane == 0 && ntok) atomicAdd(&s_tok, ntok);
 #pragma unroll
-        for (int i = 0; i < kBalPer; ++i) s_sum[warp][lane + 32 * i] = acc[i];
+        for (int i = 0; i < NP; ++i) {
+            const int x = slot_expert<VEC>(i);
+            if (x < E) s_sum[warp][x] = acc[i];
+        }
         __syncthreads();
         const int64_t slot = static_cast<int64_t>(blockIdx.x) + s;
+        const int pad = balance_pad(E);
         if (tid < E) {
             float a = 0.0f;
 #pragma unroll
             for (int w = 0; w < 8; ++w) a += s_sum[w][tid];
-            part_p[slot * E + tid] = a;
-            part_c[slot * E + tid] = s_cnt[tid];
+            part_p[slot * pad + tid] = a;
+            part_c[slot * pad + tid] = s_cnt[tid];
         }
         if (tid == 0) part_n[slot] = s_tok;
         __syncthreads();
@@ -131,24 +209,25 @@ __global__ void __launch_bounds__(256) balance_partial_kernel(
 }
 
 // Pass 2: CTA s adds the windows of sequence s (fp64, window order within each
-// of kBalGroups interleaved groups, then group order) and writes its P, counts
-// and token count; the CTA that finishes last adds the sequences' losses in
-// sequence order.
-constexpr int kBalGroups = 4;
+// of kBalGroups interleaved groups of 64 threads, four experts to a thread, then
+// group order) and writes its P, counts and token count; the CTA that finishes
+// last adds the sequences' losses in sequence order.
+constexpr int kBalGroups = 8;
+constexpr int kBalFinal = kBalGroups * kMaxExperts / 4;  // threads
 
-__global__ void __launch_bounds__(kBalGroups* kMaxExperts) balance_final_kernel(
+__global__ void __launch_bounds__(kBalFinal) balance_final_kernel(
     const float* __restrict__ part_p, const int32_t* __restrict__ part_c,
     const int32_t* __restrict__ part_n, const int32_t* __restrict__ offsets, int n_seq, int64_t T,
     int E, int k, int win, float* __restrict__ P_out, int32_t* __restrict__ counts,
     int32_t* __restrict__ tokens, double* seq_loss, uint32_t* ticket, float* __restrict__ loss,
     int32_t* status) {
-    __shared__ double s_p[kBalGroups][kMaxExperts];
-    __shared__ int32_t s_c[kBalGroups][kMaxExperts];
-    __shared__ double s_red[32];
-    __shared__ int32_t s_n[32];
+    constexpr int kWarps = kBalFinal / 32;
+    __shared__ __align__(16) double s_p[kBalGroups][kMaxExperts];
+    __shared__ __align__(16) int32_t s_c[kBalGroups][kMaxExperts];
+    __shared__ double s_red[kWarps];
+    __shared__ int32_t s_n[kWarps];
     __shared__ bool s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int e = tid % kMaxExperts, g = tid / kMaxExperts;
     ptx::grid_dep_wait();
     const int s = blockIdx.x;
     int64_t o0 = 0, o1 = T;
@@ -161,29 +240,40 @@ __global__ void __launch_bounds__(kBalGroups* kMaxExperts) balance_final_kernel(
         }
     }
     const int64_t b0 = o0 / win, b1 = o1 > o0 ? (o1 - 1) / win : b0 - 1;
-    double p = 0.0;
-    int32_t c = 0, n = 0;
-    if (e < E) {
-#pragma unroll 4
-        for (int64_t b = b0 + g; b <= b1; b += kBalGroups) {
-            p += part_p[(b + s) * E + e];
-            c += part_c[(b + s) * E + e];
+    {
+        const int g = tid / (kMaxExperts / 4), e = tid % (kMaxExperts / 4) * 4;
+        const int pad = balance_pad(E);
+        double p[4] = {0.0, 0.0, 0.0, 0.0};
+        int4 c = make_int4(0, 0, 0, 0);
+        if (e < pad) {
+#pragma unroll 8
+            for (int64_t b = b0 + g; b <= b1; b += kBalGroups) {
+                const float4 v = *reinterpret_cast<const float4*>(part_p + (b + s) * pad + e);
+                const int4 d = *reinterpret_cast<const int4*>(part_c + (b + s) * pad + e);
+                p[0] += v.x, p[1] += v.y, p[2] += v.z, p[3] += v.w;
+                c.x += d.x, c.y += d.y, c.z += d.z, c.w += d.w;
+            }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s_p[g][e + i] = p[i];
+        *reinterpret_cast<int4*>(&s_c[g][e]) = c;
     }
-    s_p[g][e] = p;
-    s_c[g][e] = c;
-    for (int64_t b = b0 + tid; b <= b1; b += blockDim.x) n += part_n[b + s];
+    int32_t n = 0;
+    for (int64_t b = b0 + tid; b <= b1; b += kBalFinal) n += part_n[b + s];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     if (lane == 0) s_n[warp] = n;
     __syncthreads();
-    n = s_n[lane];
+    n = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    for (int w = 0; w < kWarps; ++w) n += s_n[w];
     double prod = 0.0;
-    if (g == 0 && e < E) {
+    const int e = tid;
+    if (e < E) {
+        double p = 0.0;
+        int32_t c = 0;
 #pragma unroll
-        for (int i = 1; i < kBalGroups; ++i) {
+        for (int i = 0; i < kBalGroups; ++i) {
             p += s_p[i][e];
             c += s_c[i][e];
         }
@@ -200,17 +290,23 @@ __global__ void __launch_bounds__(kBalGroups* kMaxExperts) balance_final_kernel(
         double a = 0.0;
 #pragma unroll
         for (int w = 0; w < kMaxExperts / 32; ++w) a += s_red[w];
-        seq_loss[s] = a * E;
         tokens[s] = n;
-        __threadfence();
-        s_last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+        if (n_seq == 1) {
+            tokens[1] = n > 0 ? 1 : 0;
+            *loss = static_cast<float>(a * E);
+        } else {
+            seq_loss[s] = a * E;
+            __threadfence();
+            s_last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+        }
     }
+    if (n_seq == 1) return;
     __syncthreads();
     if (!s_last) return;
     __threadfence();
     double a = 0.0;
     int used = 0;
-    for (int i = tid; i < n_seq; i += blockDim.x) {
+    for (int i = tid; i < n_seq; i += kBalFinal) {
         a += __ldcg(seq_loss + i);
         used += __ldcg(tokens + i) > 0 ? 1 : 0;
     }
@@ -227,7 +323,7 @@ __global__ void __launch_bounds__(kBalGroups* kMaxExperts) balance_final_kernel(
     if (tid == 0) {
         a = 0.0;
         used = 0;
-        for (int w = 0; w < 32; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             a += s_red[w];
             used += s_n[w];
         }
@@ -236,60 +332,96 @@ __global__ void __launch_bounds__(kBalGroups* kMaxExperts) balance_final_kernel(
     }
 }
 
-// Gradient of the loss.  Each warp takes `run` consecutive tokens and keeps the
-// selection shares f of its current sequence in registers.  With
-// c = 1/E, sum_j p_j (f_j - c) + c = sum_j p_j f_j: taking the shares relative
-// to the uniform one loses nothing of a small difference f - p.f to rounding.
-__global__ void __launch_bounds__(256) balance_backward_kernel(
+// Gradient of the loss.  Each warp takes `run` consecutive tokens, kBalBatch at
+// a time, and keeps the selection shares f of its current sequence in registers.
+// With c = 1/E, sum_j p_j (f_j - c) + c = sum_j p_j f_j: taking the shares
+// relative to the uniform one loses nothing of a small difference f - p.f to
+// rounding.
+template <int NP, bool VEC>
+__global__ void __launch_bounds__(256, 2) balance_backward_kernel(
     const float* __restrict__ logits, const float* __restrict__ bias,
     const uint8_t* __restrict__ mask, const int32_t* __restrict__ offsets, int n_seq, int64_t T,
     int E, int k, int run, const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens,
     const float* __restrict__ grad, float* __restrict__ dlogits) {
-    const int lane = threadIdx.x & 31;
     const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int64_t t0 = w * run, t1 = min(T, t0 + run);
     if (t0 >= T) return;
     ptx::grid_dep_wait();
-    const int used = tokens[n_seq];
-    const float g = used > 0 ? *grad * static_cast<float>(E) / static_cast<float>(used) : 0.0f;
-    int s = offsets ? first_sequence(offsets, n_seq, t0) : 0;
-    int loaded = -1;
-    float f[kBalPer];
+    int s = -1;                    // sequence of the token at hand
+    int64_t seq0 = 0, seq1 = -1;   // its tokens; none yet
+    float f[NP];
     float scale = 0.0f;
-    for (int64_t t = t0; t < t1; ++t) {
-        if (offsets)
-            while (s < n_seq && offsets[s + 1] <= t) ++s;
-        const bool live = s < n_seq && (!offsets || offsets[s] <= t) && (!mask || mask[t]);
-        float p[kBalPer];
-        if (live) {
-            if (loaded != s) {
-                loaded = s;
-                const int n = tokens[s];
+    uint32_t bits = 0;
+    for (int64_t t = t0; t < t1; t += kBalBatch) {
+        if (((t - t0) & 31) == 0) bits = live_tokens(mask, t, t1);
+        const uint32_t live = bits >> ((t - t0) & 31);
+        float l[kBalBatch][NP];
+#pragma unroll
+        for (int u = 0; u < kBalBatch; ++u)
+            if (live >> u & 1) load_slots<NP, VEC>(logits + (t + u) * E, E, -INFINITY, l[u]);
+#pragma unroll
+        for (int u = 0; u < kBalBatch; ++u) {
+            if (t + u >= t1) break;
+            if (seq1 <= t + u) {
+                // the next sequence that ends behind this token
+                if (!offsets) {
+                    s = 0;
+                    seq1 = T;
+                } else {
+                    s = first_sequence(offsets, n_seq, t + u);
+                    seq0 = s < n_seq ? offsets[s] : T;
+                    seq1 = s < n_seq ? offsets[s + 1] : T;
+                }
+                const int n = s < n_seq ? tokens[s] : 0, used = tokens[n_seq];
                 const float inv = n > 0 ? 1.0f / (static_cast<float>(n) * k) : 0.0f;
-                scale = n > 0 ? g / static_cast<float>(n) : 0.0f;
+                scale = n > 0 ? *grad * static_cast<float>(E) /
+                                    (static_cast<float>(used) * static_cast<float>(n))
+                              : 0.0f;
                 const float c = 1.0f / static_cast<float>(E);
 #pragma unroll
-                for (int i = 0; i < kBalPer; ++i) {
-                    const int e = lane + 32 * i;
-                    f[i] = e < E ? counts[static_cast<int64_t>(s) * E + e] * inv - c : 0.0f;
+                for (int i = 0; i < NP; ++i) {
+                    const int e = slot_expert<VEC>(i);
+                    f[i] = e < E && n > 0 ? counts[static_cast<int64_t>(s) * E + e] * inv - c
+                                          : 0.0f;
                 }
             }
-            token_probs(logits + t * E, bias, E, p);
-            float dot = 0.0f;
+            if ((live >> u & 1) && seq0 <= t + u && scale != 0.0f) {
+                numerators<NP, VEC>(bias, E, l[u]);
+                float z = 0.0f, dot = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kBalPer; ++i) dot = fmaf(p[i], f[i], dot);
+                for (int i = 0; i < NP; ++i) {
+                    z += l[u][i];
+                    dot = fmaf(l[u][i], f[i], dot);
+                }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                for (int o = 16; o > 0; o >>= 1) {
+                    z += __shfl_xor_sync(0xffffffffu, z, o);
+                    dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                }
+                const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+                const float a = scale * inv, ad = a * (dot * inv);
 #pragma unroll
-            for (int i = 0; i < kBalPer; ++i) p[i] = scale * (p[i] * (f[i] - dot));
-        } else {
+                for (int i = 0; i < NP; ++i) l[u][i] *= fmaf(a, f[i], -ad);
+            } else {
 #pragma unroll
-            for (int i = 0; i < kBalPer; ++i) p[i] = 0.0f;
-        }
+                for (int i = 0; i < NP; ++i) l[u][i] = 0.0f;
+            }
+            float* out = dlogits + (t + u) * E;
+            if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < kBalPer; ++i) {
-            const int e = lane + 32 * i;
-            if (e < E) dlogits[t * E + e] = p[i];
+                for (int i = 0; i < NP; i += 4) {
+                    const int e = slot_expert<VEC>(i);
+                    if (e < E)
+                        *reinterpret_cast<float4*>(out + e) =
+                            make_float4(l[u][i], l[u][i + 1], l[u][i + 2], l[u][i + 3]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const int e = slot_expert<VEC>(i);
+                    if (e < E) out[e] = l[u][i];
+                }
+            }
         }
     }
 }

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "host_common.cuh"
 #include "internal.hpp"
@@ -165,9 +166,10 @@ int32_t run_norm_backward(const moe_problem* p, const void* dy, const void* dres
 
 constexpr int32_t kMaxSequences = 1 << 20;
 
-// Tokens per window: whole rounds of the CTA's 8 warps, about 4 windows per SM.
+// Tokens per window, a multiple of the CTA's 8 warps: at most 3 windows per SM,
+// which is what its registers hold at once.
 int balance_window(int64_t T) {
-    return static_cast<int>(8 * std::max<int64_t>(1, (T + 8 * 592 - 1) / (8 * 592)));
+    return static_cast<int>(8 * std::max<int64_t>(1, (T + 8 * 444 - 1) / (8 * 444)));
 }
 
 struct BalanceLayout {
@@ -181,12 +183,26 @@ BalanceLayout balance_layout(const moe_problem* p, int64_t n_seq) {
     const int64_t slots = std::max<int64_t>(1, (p->T + win - 1) / win) + n_seq;
     L.status = c.take(256);
     L.ticket = c.take(4);
-    L.part_p = c.take(slots * p->E * 4);
-    L.part_c = c.take(slots * p->E * 4);
+    L.part_p = c.take(slots * balance_pad(p->E) * 4);
+    L.part_c = c.take(slots * balance_pad(p->E) * 4);
     L.part_n = c.take(slots * 4);
     L.seq_loss = c.take(n_seq * 8);
     L.total = c.off;
     return L;
+}
+
+// Calls f with the kernels' experts per lane and whether they load them four at
+// a time: more than 64 experts, rows of a multiple of 4, aligned arrays.
+template <typename F>
+int32_t with_slots(int E, bool aligned, F f) {
+    if (E > 64 && E % 4 == 0 && aligned) {
+        if (E > 128) return f(std::integral_constant<int, 8>{}, std::true_type{});
+        return f(std::integral_constant<int, 4>{}, std::true_type{});
+    }
+    if (E > 128) return f(std::integral_constant<int, 8>{}, std::false_type{});
+    if (E > 64) return f(std::integral_constant<int, 4>{}, std::false_type{});
+    if (E > 32) return f(std::integral_constant<int, 2>{}, std::false_type{});
+    return f(std::integral_constant<int, 1>{}, std::false_type{});
 }
 
 int32_t check_sequences(const int32_t* offsets, int32_t n_seq) {
@@ -479,13 +495,18 @@ int32_t moe_balance_loss(const moe_problem* p, const float* logits, const float*
     int32_t* part_c = at<int32_t>(ws, L.part_c);
     int32_t* part_n = at<int32_t>(ws, L.part_n);
     uint32_t* ticket = at<uint32_t>(ws, L.ticket);
-    MOE_LAUNCH("balance_partial", s,
-               if (launch_ex(balance_partial_kernel, nwin, 256, 0, s, pdl_enabled(), logits, bias,
-                             topk_idx, token_mask, seq_offsets, static_cast<int>(n_seq), p->T,
-                             p->E, p->top_k, win, part_p, part_c, part_n, ticket, status) !=
-                   cudaSuccess) return MOE_ERR_CUDA);
+    MOE_TRY(with_slots(p->E, aligned16(logits) && aligned16(bias),
+                       [&](auto np, auto vec) -> int32_t {
+        MOE_LAUNCH("balance_partial", s,
+                   if (launch_ex(balance_partial_kernel<decltype(np)::value, decltype(vec)::value>,
+                                 nwin, 256, 0, s, pdl_enabled(), logits, bias, topk_idx,
+                                 token_mask, seq_offsets, static_cast<int>(n_seq), p->T, p->E,
+                                 p->top_k, win, part_p, part_c, part_n, ticket, status) !=
+                       cudaSuccess) return MOE_ERR_CUDA);
+        return MOE_OK;
+    }));
     MOE_LAUNCH("balance_final", s,
-               if (launch_ex(balance_final_kernel, n_seq, kBalGroups * kMaxExperts, 0, s,
+               if (launch_ex(balance_final_kernel, n_seq, kBalFinal, 0, s,
                              pdl_enabled(), static_cast<const float*>(part_p),
                              static_cast<const int32_t*>(part_c),
                              static_cast<const int32_t*>(part_n), seq_offsets,
@@ -504,16 +525,22 @@ int32_t moe_balance_loss_backward(const moe_problem* p, const float* logits, con
     if (p->T == 0) return MOE_OK;
     if (!logits || !counts || !tokens || !grad_loss || !dlogits) return MOE_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // consecutive tokens per warp: about 32 warps per SM
-    const int64_t warps = 148 * 32;
+    // consecutive tokens per warp: 16 warps per SM, which are resident at once
+    const int64_t warps = 148 * 16;
     const int run = static_cast<int>((p->T + warps - 1) / warps);
     const int grid = static_cast<int>((p->T + 8 * run - 1) / (8 * run));
-    MOE_LAUNCH("balance_backward", s,
-               if (launch_ex(balance_backward_kernel, grid, 256, 0, s, pdl_enabled(), logits, bias,
-                             token_mask, seq_offsets, static_cast<int>(n_seq), p->T, p->E,
-                             p->top_k, run, counts, tokens, grad_loss, dlogits) != cudaSuccess)
-                   return MOE_ERR_CUDA);
-    return MOE_OK;
+    return with_slots(
+        p->E, aligned16(logits) && aligned16(bias) && aligned16(dlogits),
+        [&](auto np, auto vec) -> int32_t {
+            MOE_LAUNCH(
+                "balance_backward", s,
+                if (launch_ex(balance_backward_kernel<decltype(np)::value, decltype(vec)::value>,
+                              grid, 256, 0, s, pdl_enabled(), logits, bias, token_mask,
+                              seq_offsets, static_cast<int>(n_seq), p->T, p->E, p->top_k, run,
+                              counts, tokens, grad_loss, dlogits) != cudaSuccess)
+                    return MOE_ERR_CUDA);
+            return MOE_OK;
+        });
 }
 
 int32_t moe_quantize_weights_w4(const moe_problem* p, int32_t group_size, int32_t n_experts,

@@ -126,14 +126,16 @@ def balance_backward(logits, bias, mask, offsets, counts, tokens, grad, k):
 
 
 def prob_units(logits, bias):
-    """Error of a probability in units of 2^-24: the logit plus its bias (one
-    rounding of its magnitude, and again less the maximum: an absolute error of
-    the exponent), the exponential (2), the sum of 8 + 5 terms, the quotient
-    and its product (2)."""
+    """Error of a probability in units of 2^-24, with all |logit + bias| <= big.
+    Numerator: the logit plus its bias (big), less the maximum (2 big), times
+    log2 e as fp32 (product 2 big, constant 0.5 big, in units of the natural
+    exponent) are absolute errors of the exponent; the approximate exponential is
+    stated to 2^-22: 4.  The sum of numerators carries
+    as much, and 13 additions; quotient and product: 2."""
     l = logits.to(F64) + (0 if bias is None else bias.to(F64))
     fin = l[torch.isfinite(l)]
     big = float(fin.abs().max()) if fin.numel() else 0.0
-    return 3 * big + 2 + 13 + 2 + 2 * big + 15  # the sum carries its terms' errors
+    return 2 * (5.5 * big + 4) + 15
 
 
 # ------------------------------------------------------------------ 4-bit experts
