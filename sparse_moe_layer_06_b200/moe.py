@@ -74,6 +74,10 @@ class MoEProblem:
                    num_shared=cfg.num_shared, routed_scale=cfg.routed_scale,
                    clip_limit=cfg.clip_limit, dtype=cfg.dtype)
 
+    def __getstate__(self):
+        # the fields only: the C struct that calls keep beside them stays here
+        return {k: v for k, v in self.__dict__.items() if not k.startswith("_")}
+
     def c(self) -> MoEProblemC:
         code = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}.get(self.dtype)
         if code is None:
@@ -202,27 +206,82 @@ def _check(status: int, what: str):
 
 def _run(name, problem, before, operands, workspace, stream):
     """Call entry point `name` with the problem, the plain values `before`, the
-    operands (specs, checked as _ptrs checks them, and plain values between
-    them), the workspace and its size (if there is one) and the stream.  The
-    operands lie on one device; the call is made with that device current, on
-    its current stream unless `stream` names one."""
+    operands (specs as _ptrs takes them, and plain values between them), the
+    workspace and its size (if there is one) and the stream.  The operands lie
+    on one device; the call is made with that device current, on its current
+    stream unless `stream` names one.
+
+    The smallest calls take a few microseconds on the GPU, so the checks are one
+    pass of what every valid call has in common; what fails it goes through
+    _ptrs, which says what is wrong."""
+    args = [_ref(problem), *before]
+    device = None
+    try:
+        for o in operands:
+            if type(o) is not tuple:
+                args.append(o)
+                continue
+            t = o[0]
+            if t is None and o[3]:
+                args.append(None)
+                continue
+            if t.dtype is not o[1] or t.numel() < o[4] or not t.is_contiguous():
+                break
+            d = t.get_device()
+            if d != device:
+                if device is not None or d < 0:
+                    break
+                device = d
+            args.append(t.data_ptr())
+        else:
+            if workspace is not None:
+                if workspace.get_device() != device or not workspace.is_contiguous():
+                    raise ValueError
+                args += (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+            fn = _functions.get(name) or _function(name)
+            if device != _current_device():
+                with torch.cuda.device(device):
+                    return _check(fn(*args, _stream_of(stream, device)), name)
+            return _check(fn(*args, _stream_of(stream, device)), name)
+    except (AttributeError, TypeError, ValueError):
+        pass
     specs = [o for o in operands if type(o) is tuple]
-    if workspace is not None:
+    if workspace is not None or name in _NEEDS_WORKSPACE:
         specs.append(_ws(workspace))
-    ptrs = iter(_ptrs(*specs))
-    device = specs[0][0].device
-    for s in specs:
-        if s[0] is not None and s[0].device != device:
-            raise ValueError(f"{s[2]} is on {s[0].device}, {specs[0][2]} on {device}")
-    args = [next(ptrs) if type(o) is tuple else o for o in operands]
-    if workspace is not None:
-        args += [next(ptrs), workspace.numel() * workspace.element_size()]
-    pc = problem.c()
-    with torch.cuda.device(device):
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        _check(getattr(load_library(), name)(ctypes.byref(pc), *before, *args, _stream(stream)),
-               name)
+    _ptrs(*specs)
+    given = [s for s in specs if s[0] is not None]
+    for s in given:
+        if s[0].device != given[0][0].device:
+            raise ValueError(f"{s[2]} is on {s[0].device}, {given[0][2]} on {given[0][0].device}")
+    raise TypeError(f"{name}: arguments of the wrong type")
+
+
+_NEEDS_WORKSPACE = ("moe_forward_fp8_encoded", "moe_add_rmsnorm_backward", "moe_balance_loss",
+                    "moe_experts_w4", "moe_forward_w4")
+_functions = {}
+
+
+def _function(name):
+    return _functions.setdefault(name, getattr(load_library(), name))
+
+
+def _ref(problem):
+    """Reference to the problem's C struct, made once per problem object."""
+    r = problem.__dict__.get("_c_ref")
+    if r is None:
+        r = ctypes.byref(problem.c())
+        object.__setattr__(problem, "_c_ref", r)
+    return r
+
+
+def _current_device():
+    return torch.cuda.current_device()
+
+
+def _stream_of(stream, device):
+    # (the raw handle: making a Stream object costs more than the smallest launch)
+    return (torch._C._cuda_getCurrentRawStream(device) if stream is None
+            else stream.cuda_stream)
 
 
 def moe_workspace_size(problem: MoEProblem, call: int) -> int:
@@ -341,20 +400,20 @@ def moe_forward_fp8_encoded(problem, x, x_q, x_scale, gate_w, logit_bias, expert
     """moe_forward_fp8 on rows encoded already (y_q and y_scale of moe_add_rmsnorm)."""
     T, H, E, I, k = problem.T, problem.H, problem.E, problem.I, problem.top_k
     _run("moe_forward_fp8_encoded", problem, (), (
-        _spec(x, torch.bfloat16, "x", numel=T * H),
-        _spec(x_q, torch.uint8, "x_q", numel=T * H),
-        _spec(x_scale, torch.float32, "x_scale", numel=T),
-        _spec(gate_w, torch.bfloat16, "gate_w", numel=E * H),
-        _spec(logit_bias, torch.float32, "logit_bias", optional=True, numel=E),
-        _spec(expert_q, torch.uint8, "expert_q", numel=E * 3 * I * H),
-        _spec(expert_s_gu, torch.float32, "expert_s_gu", numel=E * 2 * I),
-        _spec(expert_s_d, torch.float32, "expert_s_d", numel=E * H),
-        _spec(shared_q, torch.uint8, "shared_q", optional=True, numel=3 * I * H),
-        _spec(shared_s_gu, torch.float32, "shared_s_gu", optional=True, numel=2 * I),
-        _spec(shared_s_d, torch.float32, "shared_s_d", optional=True, numel=H),
-        _spec(out, torch.bfloat16, "out", numel=T * H),
-        _spec(topk_idx_out, torch.int32, "topk_idx_out", optional=True, numel=T * k),
-        _spec(topk_w_out, torch.float32, "topk_w_out", optional=True, numel=T * k)),
+        (x, torch.bfloat16, "x", False, T * H),
+        (x_q, torch.uint8, "x_q", False, T * H),
+        (x_scale, torch.float32, "x_scale", False, T),
+        (gate_w, torch.bfloat16, "gate_w", False, E * H),
+        (logit_bias, torch.float32, "logit_bias", True, E),
+        (expert_q, torch.uint8, "expert_q", False, E * 3 * I * H),
+        (expert_s_gu, torch.float32, "expert_s_gu", False, E * 2 * I),
+        (expert_s_d, torch.float32, "expert_s_d", False, E * H),
+        (shared_q, torch.uint8, "shared_q", True, 3 * I * H),
+        (shared_s_gu, torch.float32, "shared_s_gu", True, 2 * I),
+        (shared_s_d, torch.float32, "shared_s_d", True, H),
+        (out, torch.bfloat16, "out", False, T * H),
+        (topk_idx_out, torch.int32, "topk_idx_out", True, T * k),
+        (topk_w_out, torch.float32, "topk_w_out", True, T * k)),
         workspace, stream)
 
 
@@ -364,13 +423,13 @@ def moe_add_rmsnorm(problem, x, residual, weight, eps, residual_out, y, y_q=None
     E4M3 codes and scales that moe_forward_fp8_encoded takes."""
     T, H, dt = problem.T, problem.H, problem.dtype
     _run("moe_add_rmsnorm", problem, (), (
-        _spec(x, dt, "x", numel=T * H),
-        _spec(residual, dt, "residual", optional=True, numel=T * H),
-        _spec(weight, dt, "weight", numel=H), float(eps),
-        _spec(residual_out, dt, "residual_out", optional=True, numel=T * H),
-        _spec(y, dt, "y", optional=True, numel=T * H),
-        _spec(y_q, torch.uint8, "y_q", optional=True, numel=T * H),
-        _spec(y_scale, torch.float32, "y_scale", optional=True, numel=T)), None, stream)
+        (x, dt, "x", False, T * H),
+        (residual, dt, "residual", True, T * H),
+        (weight, dt, "weight", False, H), float(eps),
+        (residual_out, dt, "residual_out", True, T * H),
+        (y, dt, "y", True, T * H),
+        (y_q, torch.uint8, "y_q", True, T * H),
+        (y_scale, torch.float32, "y_scale", True, T)), None, stream)
 
 
 def moe_add_rmsnorm_backward(problem, dy, dresidual, h, weight, eps, dx, dweight, workspace,
@@ -378,11 +437,11 @@ def moe_add_rmsnorm_backward(problem, dy, dresidual, h, weight, eps, dx, dweight
     """Gradients of moe_add_rmsnorm; h is its residual_out."""
     T, H, dt = problem.T, problem.H, problem.dtype
     _run("moe_add_rmsnorm_backward", problem, (), (
-        _spec(dy, dt, "dy", numel=T * H),
-        _spec(dresidual, dt, "dresidual", optional=True, numel=T * H),
-        _spec(h, dt, "h", numel=T * H), _spec(weight, dt, "weight", numel=H), float(eps),
-        _spec(dx, dt, "dx", numel=T * H),
-        _spec(dweight, torch.float32, "dweight", numel=H)), workspace, stream)
+        (dy, dt, "dy", False, T * H),
+        (dresidual, dt, "dresidual", True, T * H),
+        (h, dt, "h", False, T * H), (weight, dt, "weight", False, H), float(eps),
+        (dx, dt, "dx", False, T * H),
+        (dweight, torch.float32, "dweight", False, H)), workspace, stream)
 
 
 def _sequences(seq_offsets):
@@ -415,15 +474,15 @@ def moe_balance_loss(problem, logits, logit_bias, topk_idx, token_mask, seq_offs
     token counts that its backward call takes."""
     T, E, k, n = problem.T, problem.E, problem.top_k, _sequences(seq_offsets)
     _run("moe_balance_loss", problem, (), (
-        _spec(logits, torch.float32, "logits", numel=T * E),
-        _spec(logit_bias, torch.float32, "logit_bias", optional=True, numel=E),
-        _spec(topk_idx, torch.int32, "topk_idx", numel=T * k),
-        _spec(token_mask, torch.uint8, "token_mask", optional=True, numel=T),
-        _spec(seq_offsets, torch.int32, "seq_offsets", optional=True, numel=n + 1), n,
-        _spec(loss, torch.float32, "loss", numel=1),
-        _spec(counts, torch.int32, "counts", numel=n * E),
-        _spec(tokens, torch.int32, "tokens", numel=n + 1),
-        _spec(mean_prob, torch.float32, "mean_prob", numel=n * E)), workspace, stream)
+        (logits, torch.float32, "logits", False, T * E),
+        (logit_bias, torch.float32, "logit_bias", True, E),
+        (topk_idx, torch.int32, "topk_idx", False, T * k),
+        (token_mask, torch.uint8, "token_mask", True, T),
+        (seq_offsets, torch.int32, "seq_offsets", True, n + 1), n,
+        (loss, torch.float32, "loss", False, 1),
+        (counts, torch.int32, "counts", False, n * E),
+        (tokens, torch.int32, "tokens", False, n + 1),
+        (mean_prob, torch.float32, "mean_prob", False, n * E)), workspace, stream)
 
 
 def moe_balance_loss_backward(problem, logits, logit_bias, token_mask, seq_offsets, counts, tokens,
@@ -431,14 +490,14 @@ def moe_balance_loss_backward(problem, logits, logit_bias, token_mask, seq_offse
     """Gradient of moe_balance_loss with respect to the logits."""
     T, E, n = problem.T, problem.E, _sequences(seq_offsets)
     _run("moe_balance_loss_backward", problem, (), (
-        _spec(logits, torch.float32, "logits", numel=T * E),
-        _spec(logit_bias, torch.float32, "logit_bias", optional=True, numel=E),
-        _spec(token_mask, torch.uint8, "token_mask", optional=True, numel=T),
-        _spec(seq_offsets, torch.int32, "seq_offsets", optional=True, numel=n + 1), n,
-        _spec(counts, torch.int32, "counts", numel=n * E),
-        _spec(tokens, torch.int32, "tokens", numel=n + 1),
-        _spec(grad_loss, torch.float32, "grad_loss", numel=1),
-        _spec(dlogits, torch.float32, "dlogits", numel=T * E)), None, stream)
+        (logits, torch.float32, "logits", False, T * E),
+        (logit_bias, torch.float32, "logit_bias", True, E),
+        (token_mask, torch.uint8, "token_mask", True, T),
+        (seq_offsets, torch.int32, "seq_offsets", True, n + 1), n,
+        (counts, torch.int32, "counts", False, n * E),
+        (tokens, torch.int32, "tokens", False, n + 1),
+        (grad_loss, torch.float32, "grad_loss", False, 1),
+        (dlogits, torch.float32, "dlogits", False, T * E)), None, stream)
 
 
 def moe_quantize_weights_w4(problem, group_size, w, q, scales, stream=None):
@@ -446,19 +505,18 @@ def moe_quantize_weights_w4(problem, group_size, w, q, scales, stream=None):
     bytes) and bf16 scales (n*3*I*H/group_size); n is w.shape[0]."""
     n, g, per = int(w.shape[0]), int(group_size), 3 * problem.I * problem.H
     _run("moe_quantize_weights_w4", problem, (g, n), (
-        _spec(w, problem.dtype, "w", numel=n * per),
-        _spec(q, torch.uint8, "q", numel=n * per // 2),
-        _spec(scales, torch.bfloat16, "scales", numel=n * per // max(1, g))), None, stream)
+        (w, problem.dtype, "w", False, n * per),
+        (q, torch.uint8, "q", False, n * per // 2),
+        (scales, torch.bfloat16, "scales", False, n * per // max(1, g))), None, stream)
 
 
 def _w4_specs(problem, g, expert_q, expert_scale, shared_q, shared_scale, out):
     T, H, E, per = problem.T, problem.H, problem.E, 3 * problem.I * problem.H
-    return (_spec(expert_q, torch.uint8, "expert_q", numel=E * per // 2),
-            _spec(expert_scale, torch.bfloat16, "expert_scale", numel=E * per // max(1, g)),
-            _spec(shared_q, torch.uint8, "shared_q", optional=True, numel=per // 2),
-            _spec(shared_scale, torch.bfloat16, "shared_scale", optional=True,
-                  numel=per // max(1, g)),
-            _spec(out, torch.bfloat16, "out", numel=T * H))
+    return ((expert_q, torch.uint8, "expert_q", False, E * per // 2),
+            (expert_scale, torch.bfloat16, "expert_scale", False, E * per // max(1, g)),
+            (shared_q, torch.uint8, "shared_q", True, per // 2),
+            (shared_scale, torch.bfloat16, "shared_scale", True, per // max(1, g)),
+            (out, torch.bfloat16, "out", False, T * H))
 
 
 def moe_experts_w4(problem, group_size, x, topk_idx, topk_w, expert_q, expert_scale, shared_q,
@@ -466,9 +524,9 @@ def moe_experts_w4(problem, group_size, x, topk_idx, topk_w, expert_q, expert_sc
     """The layer behind its router with 4-bit expert weights."""
     T, H, k, g = problem.T, problem.H, problem.top_k, int(group_size)
     _run("moe_experts_w4", problem, (g,), (
-        _spec(x, torch.bfloat16, "x", numel=T * H),
-        _spec(topk_idx, torch.int32, "topk_idx", numel=T * k),
-        _spec(topk_w, torch.float32, "topk_w", numel=T * k),
+        (x, torch.bfloat16, "x", False, T * H),
+        (topk_idx, torch.int32, "topk_idx", False, T * k),
+        (topk_w, torch.float32, "topk_w", False, T * k),
         *_w4_specs(problem, g, expert_q, expert_scale, shared_q, shared_scale, out)),
         workspace, stream)
 
@@ -478,12 +536,12 @@ def moe_forward_w4(problem, group_size, x, gate_w, logit_bias, expert_q, expert_
     """moe_route and moe_experts_w4 in one call."""
     T, H, E, k, g = problem.T, problem.H, problem.E, problem.top_k, int(group_size)
     _run("moe_forward_w4", problem, (g,), (
-        _spec(x, torch.bfloat16, "x", numel=T * H),
-        _spec(gate_w, torch.bfloat16, "gate_w", numel=E * H),
-        _spec(logit_bias, torch.float32, "logit_bias", optional=True, numel=E),
+        (x, torch.bfloat16, "x", False, T * H),
+        (gate_w, torch.bfloat16, "gate_w", False, E * H),
+        (logit_bias, torch.float32, "logit_bias", True, E),
         *_w4_specs(problem, g, expert_q, expert_scale, shared_q, shared_scale, out),
-        _spec(topk_idx_out, torch.int32, "topk_idx_out", optional=True, numel=T * k),
-        _spec(topk_w_out, torch.float32, "topk_w_out", optional=True, numel=T * k)),
+        (topk_idx_out, torch.int32, "topk_idx_out", True, T * k),
+        (topk_w_out, torch.float32, "topk_w_out", True, T * k)),
         workspace, stream)
 
 
