@@ -51,17 +51,18 @@ struct W4Shape {
     static constexpr int kWarps = NT == 1 ? 16 : 12;
     static constexpr int kMostLog = NT == 1 ? 4 : 2;  // log2 of the warps that share a tile
     static constexpr int kStages = 2;  // weight blocks a warp has on the way in registers
-    static constexpr int kAhead = 6;   // blocks that L2 has on the way for it
+    static constexpr int kAhead = 1;   // blocks that L2 has on the way for it
     static constexpr int kVals = 2 * NT * 4 * 32;         // fp32 sums of a tile
     static constexpr int kSumBytes = kWarps * kVals * 4;  // a buffer of them
     static constexpr int kSlack = 8 * NT * kW4RowBytes;   // rows read past the last block
 };
 
-// Sums of the token rows' limbs are kept for groups of at most 64 values, so a
-// block has w4_sums of them; words per row and block of the sums and the scale.
+// Beside a row's block stand -8 times the sums of its two limbs over each group
+// of at most 64 values (w4_sums of them: a pair of int32 each), then the scale;
+// words of that per row and block, whole 16-byte vectors.
 __host__ __device__ constexpr int w4_sums(int sub) { return sub == 4 ? 4 : 2; }
-__host__ __device__ constexpr int w4_meta_words(int sub) { return sub == 4 ? 8 : 4; }
-constexpr int kW4MaxMeta = 8;
+__host__ __device__ constexpr int w4_meta_words(int sub) { return sub == 4 ? 12 : 8; }
+constexpr int kW4MaxMeta = 12;
 
 // Rows of K values that fit beside the sums and the schedule (4 KB) in a CTA's
 // shared memory, at most 8 NT.
@@ -183,9 +184,8 @@ __device__ __forceinline__ void w4_split_block(const T* __restrict__ rows, int s
         sum_lo += __shfl_xor_sync(0xffffffffu, sum_lo, o);
     }
     if (lane % per == 0)
-        meta[lane / per] = (static_cast<uint32_t>(sum_hi) << 16) |
-                           (static_cast<uint32_t>(sum_lo) & 0xffffu);
-    if (lane == 0) meta[sums] = bad ? 0x7fc00000u : __float_as_uint(scale);
+        *reinterpret_cast<int2*>(meta + lane / per * 2) = make_int2(-8 * sum_hi, -8 * sum_lo);
+    if (lane == 0) meta[2 * sums] = bad ? 0x7fc00000u : __float_as_uint(scale);
 }
 
 template <typename T>
@@ -255,7 +255,9 @@ __device__ __forceinline__ void w4_next_round(W4Round& p, const W4Sched& sp, int
 // experts (2.9 GB).  2^log_ks warps share a tile, each with a part of its
 // blocks; their fp32 sums are added in shared memory in warp order.  The weights
 // stream through registers, kStages blocks ahead and across rounds, past L1; that
-// covers the way from L2, and a prefetch kAhead blocks further that from memory.
+// covers the way from L2, and a prefetch kAhead blocks further that from memory
+// (further ahead costs more than it hides: 445 us with 1, 449 with 2, 474 with 6,
+// 459 without).
 template <int NT, bool DOWN, int SUB>
 __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
     w4_product_kernel(const W4Args args) {
@@ -407,54 +409,41 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
             // with one column tile the two halves' accumulators of a whole block
             // fit; with two, groups of at most 64 run one half after the other
             constexpr bool kWhole = NT == 1 && SUB == 1;
-            uint32_t sum[NT][2][kSums];
-            float scale[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t* p = s_meta + m + (8 * n + j) * kMeta;
-                    const uint4 v = *reinterpret_cast<const uint4*>(p);
-                    sum[n][j][0] = v.x;
-                    sum[n][j][1] = v.y;
-                    if constexpr (SUB == 4) {
-                        sum[n][j][2] = v.z;
-                        sum[n][j][3] = v.w;
-                    }
-                    scale[n][j] = __uint_as_float(SUB == 4 ? p[4] : v.z);
-                }
-            m += cap * kMeta;
             int32_t acc[kWhole ? 2 : 1][2][NT][4];  // [half][limb hi, lo]
-            int32_t from[2][NT][4];  // -8 times the limb sums (row r + 8: 16 u, -128)
+            int32_t from[2][NT][4];  // the limb sums' multiples (row r + 8: 16 u)
             auto start = [&](int g) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const uint32_t v = sum[n][j][g];
-                        int32_t hi = static_cast<int32_t>(v) >> 16;
-                        int32_t lo = static_cast<int16_t>(v & 0xffffu);
+                        const uint32_t* p = s_meta + m + (8 * n + j) * kMeta;
+                        int2 v;
                         if constexpr (kWhole) {
-                            hi += static_cast<int32_t>(sum[n][j][1]) >> 16;
-                            lo += static_cast<int16_t>(sum[n][j][1] & 0xffffu);
+                            const int4 q = *reinterpret_cast<const int4*>(p);
+                            v = make_int2(q.x + q.z, q.y + q.w);
+                        } else {
+                            v = *reinterpret_cast<const int2*>(p + 2 * g);
                         }
-                        from[0][n][j] = -8 * hi;
-                        from[0][n][2 + j] = -128 * hi;
-                        from[1][n][j] = -8 * lo;
-                        from[1][n][2 + j] = -128 * lo;
+                        from[0][n][j] = v.x;
+                        from[0][n][2 + j] = 16 * v.x;
+                        from[1][n][j] = v.y;
+                        from[1][n][2 + j] = 16 * v.y;
                     }
             };
-            auto finish = [&](const int32_t (&a)[2][NT][4], int h, int g) {
+            // the block's sum of s (256 hi + lo), before the rows' scales
+            float part[2][NT][4];
+            auto finish = [&](const int32_t (&a)[2][NT][4], int h, int g, bool first) {
                 const uint2 s2 = s.s[g];
                 const uint32_t sw = h ? s2.y : s2.x;
                 const float2 sv = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&sw));
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        tot[h][n][i] = fmaf((i < 2 ? sv.x : sv.y) * scale[n][i & 1],
-                                            static_cast<float>(a[0][n][i] * 256 + a[1][n][i]),
-                                            tot[h][n][i]);
+                    for (int i = 0; i < 4; ++i) {
+                        const float v = static_cast<float>(a[0][n][i] * 256 + a[1][n][i]);
+                        const float w = i < 2 ? sv.x : sv.y;
+                        part[h][n][i] = first ? w * v : fmaf(w, v, part[h][n][i]);
+                    }
             };
             uint4 bv[NT][2];
             auto step = [&](int32_t (&a)[2][NT][4], int h, int k32, bool first) {
@@ -497,16 +486,32 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
                                 step(acc[0], h, 2 * k64, true);
                                 step(acc[0], h, 2 * k64 + 1, false);
                             }
-                            finish(acc[0], h, SUB == 4 ? 2 * k64 + g : (SUB == 2 ? k64 : 0));
+                            finish(acc[0], h, SUB == 4 ? 2 * k64 + g : (SUB == 2 ? k64 : 0),
+                                   k64 + g == 0);
                         }
                     }
                 }
             }
             if constexpr (kWhole) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) finish(acc[h], h, 0);
+                for (int h = 0; h < 2; ++h) finish(acc[h], h, 0, true);
             }
+            float scale[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    scale[n][j] =
+                        __uint_as_float(s_meta[m + (8 * n + j) * kMeta + 2 * kSums]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tot[h][n][i] = fmaf(scale[n][i & 1], part[h][n][i], tot[h][n][i]);
             b += cap * kW4RowBytes;
+            m += cap * kMeta;
         };
 #pragma unroll 1
         for (int kb = 0; kb < mine.n; kb += kStages) {
