@@ -272,7 +272,7 @@ int32_t launch_w4_n(const W4Args& a, int64_t max_tasks, cudaStream_t s) {
     static std::atomic<uint64_t> configured{0};
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
     if (!bit || !(configured.load() & bit)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024) !=
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) !=
             cudaSuccess)
             return MOE_ERR_CUDA;
         configured.fetch_or(bit);

@@ -33,6 +33,7 @@
 
 #include <cuda_bf16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "ptx.cuh"
@@ -64,12 +65,12 @@ __host__ __device__ constexpr int w4_sums(int sub) { return sub == 4 ? 4 : 2; }
 __host__ __device__ constexpr int w4_meta_words(int sub) { return sub == 4 ? 12 : 8; }
 constexpr int kW4MaxMeta = 12;
 
-// Rows of K values that fit beside the sums and the schedule (4 KB) in a CTA's
+// Rows of K values that fit beside the sums and the schedule (5 KB) in a CTA's
 // shared memory, at most 8 NT.
 template <int NT>
 int w4_rows_cap(int64_t K, int sub) {
     const int64_t row = K / kW4Block * (kW4RowBytes + 4 * w4_meta_words(sub));
-    const int64_t cap = (222 * 1024 - 2 * W4Shape<NT>::kSumBytes - W4Shape<NT>::kSlack) / row;
+    const int64_t cap = (220 * 1024 - 2 * W4Shape<NT>::kSumBytes - W4Shape<NT>::kSlack) / row;
     return static_cast<int>(cap < 8 * NT ? cap : 8 * NT);
 }
 
@@ -204,6 +205,56 @@ struct W4Sched {
         rows[kMaxSegments];
 };
 
+// Shares of the run that chunks of one and of two column tiles are worth: with
+// equal shares the CTAs that met two large chunks set the time of a T = 256 batch.
+constexpr int kW4CostOne = 5, kW4CostTwo = 9;
+
+// cost[g] = sum of the chunk costs of the segments before g, by one warp.
+__device__ __forceinline__ void w4_cost_prefix(const W4Sched& sp, int nseg, int cap,
+                                               int32_t* cost) {
+    const int lane = threadIdx.x & 31;
+    int before = 0;
+    for (int s0 = 0; s0 < nseg; s0 += 32) {
+        const int s = s0 + lane;
+        int v = 0;
+        if (s < nseg && sp.rows[s] > 0) {
+            const int full = sp.prefix[s + 1] - sp.prefix[s] - 1;  // chunks before the last
+            v = full * (cap <= 8 ? kW4CostOne : kW4CostTwo) +
+                (sp.rows[s] - full * cap <= 8 ? kW4CostOne : kW4CostTwo);
+        }
+        int x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (s < nseg) cost[s] = before + x - v;
+        before += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) cost[nseg] = before;
+}
+
+// First task that starts at place x or behind it, of cost[nseg] * tiles places.
+__device__ __forceinline__ int64_t w4_task_at(const W4Sched& sp, const int32_t* cost, int nseg,
+                                              int cap, int tiles, int64_t x) {
+    if (x >= static_cast<int64_t>(cost[nseg]) * tiles)
+        return static_cast<int64_t>(sp.prefix[nseg]) * tiles;
+    int lo = 0, hi = nseg - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (static_cast<int64_t>(cost[mid]) * tiles <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    x -= static_cast<int64_t>(cost[lo]) * tiles;
+    const int chunks = sp.prefix[lo + 1] - sp.prefix[lo];
+    const int full = cap <= 8 ? kW4CostOne : kW4CostTwo;
+    const int j = static_cast<int>(min(x / (static_cast<int64_t>(full) * tiles),
+                                       static_cast<int64_t>(chunks - 1)));
+    x -= static_cast<int64_t>(j) * full * tiles;
+    const int own = sp.rows[lo] - j * cap <= 8 ? kW4CostOne : kW4CostTwo;
+    return static_cast<int64_t>(sp.prefix[lo] + j) * tiles + (x + own - 1) / own;
+}
+
 // A round of a CTA: `tiles` tiles from `tile` on of one chunk of rows (chunk
 // number `group` of the launch), each shared by 2^log_ks warps.
 struct W4Round {
@@ -287,10 +338,21 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
     }
     __syncthreads();
     // this CTA's run of tasks
-    const int groups = sp.prefix[args.nseg];
-    const int64_t total = static_cast<int64_t>(groups) * args.tiles;
-    const int64_t begin = total * blockIdx.x / gridDim.x;
-    const int run = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x - begin);
+    int64_t begin, end;
+    if constexpr (NT == 1) {
+        const int64_t total = static_cast<int64_t>(sp.prefix[args.nseg]) * args.tiles;
+        begin = total * blockIdx.x / gridDim.x;
+        end = total * (blockIdx.x + 1) / gridDim.x;
+    } else {
+        __shared__ int32_t cost[kMaxSegments + 1];
+        if (warp == 0) w4_cost_prefix(sp, args.nseg, cap, cost);
+        __syncthreads();
+        const int64_t total = static_cast<int64_t>(cost[args.nseg]) * args.tiles;
+        begin = w4_task_at(sp, cost, args.nseg, cap, args.tiles, total * blockIdx.x / gridDim.x);
+        end = w4_task_at(sp, cost, args.nseg, cap, args.tiles,
+                         total * (blockIdx.x + 1) / gridDim.x);
+    }
+    const int run = static_cast<int>(end - begin);
     if (run == 0) {
         if constexpr (DOWN) ptx::grid_dep_wait();
         return;
@@ -404,16 +466,18 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
         const int kb0 = (warp & ((1 << cur.log_ks) - 1)) * nkb >> cur.log_ks;
         uint32_t b = (kb0 * cap + r) * kW4RowBytes + (c ^ ((r & 1) * 4)) * 16;
         uint32_t m = (kb0 * cap + 2 * c) * kMeta;
-        auto block = [&](const W4Stage<SUB>& s) {
+        // one weight block against N column tiles (those that the chunk has rows for)
+        auto block = [&](auto tiles, const W4Stage<SUB>& s) {
+            constexpr int N = decltype(tiles)::value;
             constexpr int kSums = w4_sums(SUB);
             // with one column tile the two halves' accumulators of a whole block
             // fit; with two, groups of at most 64 run one half after the other
-            constexpr bool kWhole = NT == 1 && SUB == 1;
-            int32_t acc[kWhole ? 2 : 1][2][NT][4];  // [half][limb hi, lo]
-            int32_t from[2][NT][4];  // the limb sums' multiples (row r + 8: 16 u)
+            constexpr bool kWhole = N == 1 && SUB == 1;
+            int32_t acc[kWhole ? 2 : 1][2][N][4];  // [half][limb hi, lo]
+            int32_t from[2][N][4];  // the limb sums' multiples (row r + 8: 16 u)
             auto start = [&](int g) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < N; ++n)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t* p = s_meta + m + (8 * n + j) * kMeta;
@@ -431,13 +495,13 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
                     }
             };
             // the block's sum of s (256 hi + lo), before the rows' scales
-            float part[2][NT][4];
-            auto finish = [&](const int32_t (&a)[2][NT][4], int h, int g, bool first) {
+            float part[2][N][4];
+            auto finish = [&](const int32_t (&a)[2][N][4], int h, int g, bool first) {
                 const uint2 s2 = s.s[g];
                 const uint32_t sw = h ? s2.y : s2.x;
                 const float2 sv = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&sw));
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < N; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float v = static_cast<float>(a[0][n][i] * 256 + a[1][n][i]);
@@ -445,13 +509,13 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
                         part[h][n][i] = first ? w * v : fmaf(w, v, part[h][n][i]);
                     }
             };
-            uint4 bv[NT][2];
-            auto step = [&](int32_t (&a)[2][NT][4], int h, int k32, bool first) {
+            uint4 bv[N][2];
+            auto step = [&](int32_t (&a)[2][N][4], int h, int k32, bool first) {
                 const uint32_t w0 = s.a[h][2 * k32], w1 = s.a[h][2 * k32 + 1];
                 const uint32_t f[4] = {w0 & 0x0f0f0f0fu, w0 & 0xf0f0f0f0u, w1 & 0x0f0f0f0fu,
                                        w1 & 0xf0f0f0f0u};
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < N; ++n)
 #pragma unroll
                     for (int l = 0; l < 2; ++l)
                         mma_u8s8(a[l][n], f, (k32 & 1) ? bv[n][l].z : bv[n][l].x,
@@ -462,7 +526,7 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
 #pragma unroll
             for (int k64 = 0; k64 < 2; ++k64) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < N; ++n)
 #pragma unroll
                     for (int l = 0; l < 2; ++l)
                         // (piece 8 k64 + 4 l + c, its bit 2 flipped in odd rows)
@@ -496,9 +560,9 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) finish(acc[h], h, 0, true);
             }
-            float scale[NT][2];
+            float scale[N][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < N; ++n)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     scale[n][j] =
@@ -506,26 +570,30 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < N; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         tot[h][n][i] = fmaf(scale[n][i & 1], part[h][n][i], tot[h][n][i]);
             b += cap * kW4RowBytes;
             m += cap * kMeta;
         };
+        auto blocks = [&](auto tiles) {
 #pragma unroll 1
-        for (int kb = 0; kb < mine.n; kb += kStages) {
+            for (int kb = 0; kb < mine.n; kb += kStages) {
 #pragma unroll
-            for (int i = 0; i < kStages; ++i) {
-                if (kb + i < mine.n) {
-                    const int ahead = kb + i + kStages + S::kAhead;
-                    if (ahead < mine.n) prefetch(mine, ahead);
-                    else if (more) prefetch(then, ahead - mine.n);
-                    block(st[i]);
-                    load(st[i], mine, kb + i + kStages);
+                for (int i = 0; i < kStages; ++i) {
+                    if (kb + i < mine.n) {
+                        const int ahead = kb + i + kStages + S::kAhead;
+                        if (ahead < mine.n) prefetch(mine, ahead);
+                        else if (more) prefetch(then, ahead - mine.n);
+                        block(tiles, st[i]);
+                        load(st[i], mine, kb + i + kStages);
+                    }
                 }
             }
-        }
+        };
+        if (NT == 1 || cur.nrows <= 8) blocks(std::integral_constant<int, 1>{});
+        else blocks(std::integral_constant<int, NT>{});
         float* sums = s_sum[buffer][warp];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
