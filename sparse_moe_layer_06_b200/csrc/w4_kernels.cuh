@@ -207,7 +207,7 @@ struct W4Sched {
 
 // Shares of the run that chunks of one and of two column tiles are worth: with
 // equal shares the CTAs that met two large chunks set the time of a T = 256 batch.
-constexpr int kW4CostOne = 5, kW4CostTwo = 9;
+constexpr int kW4CostOne = 5, kW4CostTwo = 8;
 
 // cost[g] = sum of the chunk costs of the segments before g, by one warp.
 __device__ __forceinline__ void w4_cost_prefix(const W4Sched& sp, int nseg, int cap,
@@ -470,10 +470,11 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
         auto block = [&](auto tiles, const W4Stage<SUB>& s) {
             constexpr int N = decltype(tiles)::value;
             constexpr int kSums = w4_sums(SUB);
-            // with one column tile the two halves' accumulators of a whole block
-            // fit; with two, groups of at most 64 run one half after the other
-            constexpr bool kWhole = N == 1 && SUB == 1;
-            int32_t acc[kWhole ? 2 : 1][2][N][4];  // [half][limb hi, lo]
+            // with one column tile the accumulators of both halves fit, a whole
+            // block long where that is a group; with two, the halves of a group of
+            // at most 64 run one after the other
+            constexpr bool kBoth = N == 1, kWhole = kBoth && SUB == 1;
+            int32_t acc[kBoth ? 2 : 1][2][N][4];  // [half][limb hi, lo]
             int32_t from[2][N][4];  // the limb sums' multiples (row r + 8: 16 u)
             auto start = [&](int g) {
 #pragma unroll
@@ -541,17 +542,28 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
                 } else {
 #pragma unroll
                     for (int g = 0; g < (SUB == 4 ? 2 : 1); ++g) {
-                        start(SUB == 4 ? 2 * k64 + g : k64);
+                        const int sum = SUB == 4 ? 2 * k64 + g : k64;
+                        const int scale_of = SUB == 1 ? 0 : sum;
+                        constexpr int kSteps = SUB == 4 ? 1 : 2;
+                        start(sum);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            if constexpr (SUB == 4) {
-                                step(acc[0], h, 2 * k64 + g, true);
+                            if constexpr (kBoth) {
+                                if (h) continue;
+#pragma unroll
+                                for (int kk = 0; kk < kSteps; ++kk)
+#pragma unroll
+                                    for (int x = 0; x < 2; ++x)
+                                        step(acc[x], x, 2 * k64 + g + kk, kk == 0);
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+                                    finish(acc[x], x, scale_of, k64 + g == 0);
                             } else {
-                                step(acc[0], h, 2 * k64, true);
-                                step(acc[0], h, 2 * k64 + 1, false);
+#pragma unroll
+                                for (int kk = 0; kk < kSteps; ++kk)
+                                    step(acc[0], h, 2 * k64 + g + kk, kk == 0);
+                                finish(acc[0], h, scale_of, k64 + g == 0);
                             }
-                            finish(acc[0], h, SUB == 4 ? 2 * k64 + g : (SUB == 2 ? k64 : 0),
-                                   k64 + g == 0);
                         }
                     }
                 }
