@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
     ptx::cp_async_wait_all();
     __syncthreads();
 
-    for (int buffer = 0;; buffer ^= 1) {
+    for (int buffer = 0;;) {
         const bool more = cur.left > 0;
         if (more) {
             next = cur;
@@ -606,13 +606,49 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
         };
         if (NT == 1 || cur.nrows <= 8) blocks(std::integral_constant<int, 1>{});
         else blocks(std::integral_constant<int, NT>{});
-        float* sums = s_sum[buffer][warp];
+        // (the value of lane 4r + c, index i: row r + 8 (i / 2) of half h, column
+        // 8n + 2c + i % 2; row r + 8 carries 16 u)
+        auto store = [&](float g, float u, int tile, int h, int n, int i) {
+            const int col = 8 * n + 2 * c + (i & 1);
+            if (col >= cur.nrows) return;
+            const int64_t row = sp.out_row0[cur.seg] + cur.row0 + col;
+            if (i >= 2) {
+                g *= 0.0625f;
+                u *= 0.0625f;
+            }
+            if constexpr (!DOWN) {
+                // compare-select clamp: NaN passes through
+                g = g > args.clip ? args.clip : (g < -args.clip ? -args.clip : g);
+                u = u > args.clip ? args.clip : (u < -args.clip ? -args.clip : u);
+                args.out[row * args.ld + tile * 16 + (i >> 1) * 8 + r] =
+                    g / (1.0f + __expf(-g)) * u;
+            } else {
+                const float wt = row < args.routed_rows ? args.row_w[row] : 1.0f;
+                args.out[row * args.ld + tile * 32 + h * 16 + (i >> 1) * 8 + r] = wt * g;
+            }
+        };
+        // a tile of one warp's own needs neither the sums nor the barrier
+        const int ks = 1 << cur.log_ks, slot = warp >> cur.log_ks, part = warp & (ks - 1);
+        if (ks == 1) {
+            if (slot < cur.tiles) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < (DOWN ? 2 : 1); ++h)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sums[((h * NT + n) * 4 + i) * 32 + lane] = tot[h][n][i];
+                        for (int i = 0; i < 4; ++i)
+                            store(tot[h][n][i], tot[1][n][i], cur.tile + slot, h, n, i);
+            }
+        } else {
+            float* sums = s_sum[buffer][warp];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sums[((h * NT + n) * 4 + i) * 32 + lane] = tot[h][n][i];
+        }
         // the next round's first weights are on their way before this one is
         // added up, and its rows while it is
         const bool other_rows = more && next.group != cur.group;
@@ -621,40 +657,21 @@ __global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
 #pragma unroll
             for (int i = 0; i < kStages; ++i) load(st[i], mine, i);
         }
-        // (two buffers of sums in turn: the barrier of the next round lies between
-        // this round's reads and the writes of the round after)
-        __syncthreads();
+        // (two buffers of sums in turn: the barrier of the next round that uses one
+        // lies between this round's reads and the writes of the one after)
+        if (ks > 1 || other_rows) __syncthreads();
         if (other_rows) fetch_rows(next);
-        const int cur_slot = warp >> cur.log_ks, part = warp & ((1 << cur.log_ks) - 1);
-        if (cur_slot < cur.tiles) {
-            // lane 4r + c, value i: row r + 8 (i / 2) of half h, column 8n + 2c + i % 2
-            const int ks = 1 << cur.log_ks, tile = cur.tile + cur_slot;
-            const float(*from)[kVals] = &s_sum[buffer][cur_slot << cur.log_ks];
+        if (ks > 1) {
+            const float(*from)[kVals] = &s_sum[buffer][slot << cur.log_ks];
+            buffer ^= 1;
             constexpr int kOut = DOWN ? kVals : kVals / 2;
-            for (int v = part * 32 + lane; v < kOut; v += ks * 32) {
-                const int i = (v >> 5) & 3, n = (v >> 7) % NT, h = v / (kVals / 2);
-                const int col = 8 * n + 2 * c + (i & 1);
-                if (col >= cur.nrows) continue;
+            for (int v = slot < cur.tiles ? part * 32 + lane : kOut; v < kOut; v += ks * 32) {
                 float g = 0.0f, u = 0.0f;
                 for (int w = 0; w < ks; ++w) {
                     g += from[w][v];
                     if constexpr (!DOWN) u += from[w][v + kVals / 2];
                 }
-                const int64_t row = sp.out_row0[cur.seg] + cur.row0 + col;
-                if (i >= 2) {  // row r + 8 carries 16 u
-                    g *= 0.0625f;
-                    u *= 0.0625f;
-                }
-                if constexpr (!DOWN) {
-                    // compare-select clamp: NaN passes through
-                    g = g > args.clip ? args.clip : (g < -args.clip ? -args.clip : g);
-                    u = u > args.clip ? args.clip : (u < -args.clip ? -args.clip : u);
-                    args.out[row * args.ld + tile * 16 + (i >> 1) * 8 + r] =
-                        g / (1.0f + __expf(-g)) * u;
-                } else {
-                    const float wt = row < args.routed_rows ? args.row_w[row] : 1.0f;
-                    args.out[row * args.ld + tile * 32 + h * 16 + (i >> 1) * 8 + r] = wt * g;
-                }
+                store(g, u, cur.tile + slot, v / (kVals / 2), (v >> 7) % NT, (v >> 5) & 3);
             }
         }
         if (!more) break;
