@@ -87,6 +87,33 @@ def test_eps_dominates_tiny_rows_and_zero_eps(dtype):
         ref.assert_within(y, yr, ref.norm_y_bound(yr, dtype), f"eps {eps}")
 
 
+# several rows per CTA pass through the ring of a wide row's copies, the last CTAs
+# with one row fewer; one, two and three vectors per thread
+@pytest.mark.parametrize("dtype,T,H", [(BF, 2503, 1152), (BF, 2503, 2112), (BF, 2503, 9024),
+                                       (BF, 445, 16384), (F32, 2503, 1152), (F32, 2503, 3136),
+                                       (F32, 445, 16384)])
+def test_many_wide_rows(dtype, T, H):
+    x, res = draw(T, H, dtype, 50), draw(T, H, dtype, 51, 3.0)
+    w = draw(1, H, dtype, 52, 0.2)[0] + 1
+    ro, y, q, s = run_norm(x, res, w, 1e-6, codes=True)
+    sr, yr, _ = ref.norm(x, res, w, 1e-6)
+    ref.assert_within(y, yr, ref.norm_y_bound(yr, dtype), "y")
+    ref.assert_within(ro, sr, sr.abs() * (ref.HALF_STEP[dtype] + 2.0 ** -24 * 1.01), "residual")
+    want = (y.float() / s[:, None]).to(torch.float8_e4m3fn)
+    assert torch.equal(q, want.view(torch.uint8))
+    dy, dres = draw(T, H, dtype, 53, 0.01), draw(T, H, dtype, 54, 0.01)
+    dx, dw = run_backward(dy, dres, x, w, 1e-6)
+    dxr, dwr, mx, mw = ref.norm_backward(dy, dres, x, w, 1e-6)
+    ref.assert_within(dx, dxr, ref.norm_dx_bound(dxr, mx, dtype), "dx")
+    ref.assert_within(dw, dwr, ref.norm_dw_bound(mw, T), "dweight")
+    # the same rows in place, and alone
+    xd, rd = x.to(DEV), res.to(DEV)
+    moe.moe_add_rmsnorm(problem(T, H, dtype), xd, rd, w.to(DEV), 1e-6, rd, xd)
+    assert torch.equal(xd, y) and torch.equal(rd, ro)
+    alone = run_norm(x[T - 1:], res[T - 1:], w, 1e-6)[1]
+    assert torch.equal(alone[0], y[T - 1])
+
+
 def test_infinities_and_nans_stay_in_their_rows():
     x = draw(4, 512, BF, 9)
     clean = run_norm(x, None, torch.ones(512, dtype=BF), 1e-6, codes=True)
