@@ -264,13 +264,15 @@ W4Layout w4_layout(const moe_problem* p, bool with_route) {
 int w4_column_tiles(double mean_rows) { return mean_rows <= 7.0 ? 1 : 2; }
 
 int w4_cap(int nt, int64_t K, int sub) {
-    return nt == 1 ? w4_rows_cap<1>(K, sub) : w4_rows_cap<2>(K, sub);
+    if (sub == 1) return nt == 1 ? w4_rows_cap<1, 1>(K) : w4_rows_cap<2, 1>(K);
+    if (sub == 2) return nt == 1 ? w4_rows_cap<1, 2>(K) : w4_rows_cap<2, 2>(K);
+    return nt == 1 ? w4_rows_cap<1, 4>(K) : w4_rows_cap<2, 4>(K);
 }
 
 template <int NT, bool DOWN, int SUB>
 int32_t launch_w4_n(const W4Args& a, int64_t max_tasks, cudaStream_t s) {
     auto kern = w4_product_kernel<NT, DOWN, SUB>;
-    constexpr int threads = W4Shape<NT>::kWarps * 32;
+    constexpr int threads = W4Shape<NT, SUB>::kWarps * 32;
     int dev = 0;
     cudaGetDevice(&dev);
     static std::atomic<uint64_t> configured{0};
@@ -281,7 +283,7 @@ int32_t launch_w4_n(const W4Args& a, int64_t max_tasks, cudaStream_t s) {
             return MOE_ERR_CUDA;
         configured.fetch_or(bit);
     }
-    const int smem = 2 * W4Shape<NT>::kSumBytes + W4Shape<NT>::kSlack +
+    const int smem = 2 * W4Shape<NT, SUB>::kSumBytes + W4Shape<NT, SUB>::kSlack +
                      a.K / kW4Block * a.cap * (kW4RowBytes + 4 * w4_meta_words(SUB));
     const int grid =
         static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sm_count(), max_tasks)));

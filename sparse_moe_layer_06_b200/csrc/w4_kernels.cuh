@@ -45,12 +45,14 @@ constexpr int kW4BlockBytes = 2048; // codes of a pair tile's block
 constexpr int kW4RowBytes = 256;    // limbs of a row's block
 constexpr int kW4MaxK = 65536;      // longest contraction (a row's limbs: 147 KB)
 
-// Shape of a launch whose tasks have up to 8 NT rows: one CTA per SM.  One column
-// tile leaves 128 registers a thread and so 16 warps, two take up to 168.
-template <int NT>
+// Shape of a launch whose tasks have up to 8 NT rows, in groups of 128 / SUB: one
+// CTA per SM.  One column tile leaves 128 registers a thread and so 16 warps; two,
+// or the scales of groups of 32, take up to 168 (110 and 63 us with 12 warps, 121
+// and 69 with 16, for 37 tokens of 32 experts of 7168 x 2048).
+template <int NT, int SUB>
 struct W4Shape {
-    static constexpr int kWarps = NT == 1 ? 16 : 12;
-    static constexpr int kMostLog = NT == 1 ? 4 : 2;  // log2 of the warps that share a tile
+    static constexpr int kWarps = NT == 1 && SUB < 4 ? 16 : 12;
+    static constexpr int kMostLog = kWarps == 16 ? 4 : 3;  // log2 of the warps that share a tile
     static constexpr int kStages = 2;  // weight blocks a warp has on the way in registers
     static constexpr int kAhead = 1;   // blocks that L2 has on the way for it
     static constexpr int kVals = 2 * NT * 4 * 32;         // fp32 sums of a tile
@@ -67,10 +69,11 @@ constexpr int kW4MaxMeta = 12;
 
 // Rows of K values that fit beside the sums and the schedule (5 KB) in a CTA's
 // shared memory, at most 8 NT.
-template <int NT>
-int w4_rows_cap(int64_t K, int sub) {
-    const int64_t row = K / kW4Block * (kW4RowBytes + 4 * w4_meta_words(sub));
-    const int64_t cap = (220 * 1024 - 2 * W4Shape<NT>::kSumBytes - W4Shape<NT>::kSlack) / row;
+template <int NT, int SUB>
+int w4_rows_cap(int64_t K) {
+    using S = W4Shape<NT, SUB>;
+    const int64_t row = K / kW4Block * (kW4RowBytes + 4 * w4_meta_words(SUB));
+    const int64_t cap = (220 * 1024 - 2 * S::kSumBytes - S::kSlack) / row;
     return static_cast<int>(cap < 8 * NT ? cap : 8 * NT);
 }
 
@@ -310,9 +313,9 @@ __device__ __forceinline__ void w4_next_round(W4Round& p, const W4Sched& sp, int
 // (further ahead costs more than it hides: 445 us with 1, 449 with 2, 474 with 6,
 // 459 without).
 template <int NT, bool DOWN, int SUB>
-__global__ void __launch_bounds__(W4Shape<NT>::kWarps * 32, 1)
+__global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
     w4_product_kernel(const W4Args args) {
-    using S = W4Shape<NT>;
+    using S = W4Shape<NT, SUB>;
     constexpr int kWarps = S::kWarps, kStages = S::kStages, kVals = S::kVals;
     constexpr int kMeta = w4_meta_words(SUB);
     extern __shared__ __align__(128) uint8_t s_dyn[];
