@@ -385,8 +385,8 @@ int32_t moe_add_rmsnorm_backward(const moe_problem* problem, const void* dy,
  * probability 0; a token whose logits are all -inf has probability 0
  * throughout.  Sums are taken in a fixed order (reproducible).  Offsets out of
  * order and experts out of range set MOE_ERR_BAD_INDEX in the error word (such
- * a sequence counts as empty, such a selection not at all).  1 <= n_seq <=
- * 2^20.  Workspace: moe_balance_loss_workspace_size(problem, n_seq)
+ * a sequence counts as empty, such a selection not at all; where offsets go
+ * down, what the other sequences give is not defined).  1 <= n_seq <= 2^20.  Workspace: moe_balance_loss_workspace_size(problem, n_seq)
  * (MOE_CALL_BALANCE_LOSS sizes it for n_seq = 1).
  */
 size_t moe_balance_loss_workspace_size(const moe_problem* problem, int32_t n_seq);
@@ -403,7 +403,7 @@ int32_t moe_balance_loss(const moe_problem* problem, const float* logits, const 
  *   f[e] = counts[s,e] / (n_s top_k), s the token's sequence
  * and 0 for tokens that do not count.  counts and tokens are those of
  * moe_balance_loss on the same sequences and mask; grad_loss [1] fp32 device;
- * dlogits [T, E] fp32 device, out.  No workspace.
+ * dlogits [T, E] fp32 device, out, not the logits' own buffer.  No workspace.
  */
 int32_t moe_balance_loss_backward(const moe_problem* problem, const float* logits,
                                   const float* logit_bias, const uint8_t* token_mask,
@@ -416,8 +416,16 @@ int32_t moe_balance_loss_backward(const moe_problem* problem, const float* logit
  * checkpoint with 4-bit weights; the pages give no format).  A weight is
  * (u - 8) * s: u its 4-bit code, s the bf16 scale of its group of group_size
  * (32, 64 or 128) consecutive weights along the contraction (H for gate and
- * up, I for down).  Activations stay bf16, sums fp32.  H and I must be
- * multiples of 128.
+ * up, I for down).  H and I must be multiples of 128, at most 65536.
+ *
+ * Numerics.  The products take each token row (and each row of h, which is
+ * fp32) in blocks of 128 values with a power-of-two scale a and 16-bit
+ * integers: bf16 values down to 2^-7 of the block's largest magnitude are exact,
+ * any other value is off by at most a/2, 2^-14.9 of that magnitude.  The integer
+ * sums of a group are exact; scaled, they are added in fp32.  A row with a value
+ * that is not finite gives NaN.  Group scales are for weights of ordinary size:
+ * one above 2^90 can overflow an fp32 sum that smaller activations would bring
+ * back into range.
  *
  * Packed layout, per expert: 3*I*H/2 bytes of codes and 3*I*H/group_size
  * scales, the gate/up part (I*H bytes, 2*I*H/group_size scales) before the

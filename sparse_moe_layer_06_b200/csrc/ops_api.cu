@@ -446,6 +446,7 @@ int32_t moe_add_rmsnorm(const moe_problem* p, const void* x, const void* residua
         !aligned16(y) || !aligned16(y_q))
         return MOE_ERR_INVALID_ARG;
     if (p->T == 0) return MOE_OK;
+    if (residual_out && residual_out == y) return MOE_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p->dtype == MOE_BF16)
         return run_norm<__nv_bfloat16>(p, x, residual, weight, eps, residual_out, y, y_q, y_scale,
@@ -529,7 +530,8 @@ int32_t moe_balance_loss_backward(const moe_problem* p, const float* logits, con
     MOE_TRY(check_problem(p));
     MOE_TRY(check_sequences(seq_offsets, n_seq));
     if (p->T == 0) return MOE_OK;
-    if (!logits || !counts || !tokens || !grad_loss || !dlogits) return MOE_ERR_INVALID_ARG;
+    if (!logits || !counts || !tokens || !grad_loss || !dlogits || dlogits == logits)
+        return MOE_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // consecutive tokens per warp: 16 warps per SM, which are resident at once
     const int64_t warps = 148 * 16;

@@ -377,17 +377,6 @@ __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// The two E4M3 codes of e4m3x2 as fp32: {low byte, high byte}.
-__device__ __forceinline__ float2 e4m3x2_f32(uint32_t codes) {
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(codes)));
-    float2 f;
-    asm("{.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}"
-        : "=f"(f.x), "=f"(f.y)
-        : "r"(h2));
-    return f;
-}
-
 // Arrive once on `bar` when every tcgen05.mma issued so far by this thread has
 // completed (which also releases the shared-memory operands they read).
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {

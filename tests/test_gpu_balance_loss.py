@@ -189,3 +189,35 @@ def test_reproducible_and_empty_batch():
     assert float(loss[0]) == 0 and (counts == 0).all() and tokens.tolist() == [0, 0]
     assert (P == 0).all()
     assert run_backward(e[0], None, None, None, counts, tokens, 1.0, 2).numel() == 0
+
+
+def test_many_sequences():
+    # more than 1024: three rounds of the search for a window's first sequence
+    g = torch.Generator().manual_seed(11)
+    cuts = torch.randint(0, 3001, (2500,), generator=g).sort().values.tolist()
+    check(*draw(3000, 16, 2, 12, 0.6, 0.2), [0] + cuts + [3000])
+
+
+def test_tokens_past_the_32_bit_offset():
+    # the tokens of the last sequence lie behind element 2^31 of the logits; the
+    # others are masked, so their (uninitialised) logits are not read
+    T, E, k, n = (1 << 23) + 777, 256, 2, 900
+    logits, bias, idx, _ = draw(n, E, k, 13, 0.6)
+    lg = torch.empty(T, E, device=DEV)
+    lg[T - n:] = logits.to(DEV)
+    ix = torch.zeros(T, k, dtype=torch.int32, device=DEV)
+    ix[T - n:] = idx.to(DEV)
+    mask = torch.zeros(T, dtype=torch.uint8, device=DEV)
+    mask[T - n:] = 1
+    offsets = [0, 100, T - n, T]
+    loss, counts, tokens, P = run_loss(lg, bias, ix, mask, offsets)
+    rl, rc, rt, rP = ref.balance_loss(logits, bias, idx, None, None, k)
+    units = ref.prob_units(logits, bias)
+    assert torch.equal(counts[2].cpu(), rc[0]) and tokens.tolist() == [0, 0, n, 1]
+    # (a warp's share of a window is over 2000 tokens here, so it adds up to n of them)
+    ref.assert_within(P[2], rP[0], rP[0] * (units + n + 8) * 2.0 ** -24, "mean_prob")
+    assert abs(float(loss[0]) - rl) <= abs(rl) * (units + n + 10) * 2.0 ** -24
+    dl = run_backward(lg, bias, mask, offsets, counts, tokens, 0.37, k)
+    d, mag = ref.balance_backward(logits, bias, None, None, rc, rt, 0.37, k)
+    ref.assert_within(dl[T - n:], d, mag * (2 * units + 24) * 2.0 ** -24, "dlogits")
+    assert not dl[:T - n].any()

@@ -231,3 +231,25 @@ def test_on_a_side_stream():
     moe.moe_add_rmsnorm(problem(T, H, BF), x, None, w, 1e-6, None, y, stream=side)
     side.synchronize()
     assert torch.equal(y, want)
+
+
+def test_rows_past_the_32_bit_offset():
+    # 2^31 elements and more: the last rows are those of a small batch
+    T, H = 131075, 16384
+    g = torch.Generator(device=DEV).manual_seed(60)
+    tail = torch.randn(5, H, generator=g, device=DEV).to(BF)
+    w = torch.rand(H, generator=g, device=DEV).to(BF)
+    x = torch.zeros(T, H, dtype=BF, device=DEV)
+    x[T - 5:] = tail
+    y = torch.empty_like(x)
+    moe.moe_add_rmsnorm(problem(T, H, BF), x, x, w, 1e-6, None, y)
+    small = run_norm(tail, tail, w, 1e-6)[1]
+    assert torch.equal(y[T - 5:], small) and not y[:T - 5].any()
+    p = problem(T, H, BF)
+    dw = torch.empty(H, device=DEV)
+    moe.moe_add_rmsnorm_backward(p, x, None, x, w, 1e-6, y, dw,
+                                 moe.alloc_workspace(p, moe.MOE_CALL_ADD_RMSNORM_BACKWARD))
+    dx, _ = run_backward(tail, None, tail, w, 1e-6)
+    assert torch.equal(y[T - 5:], dx) and not y[:T - 5].any()
+    _, dwr, _, mw = ref.norm_backward(tail.cpu(), None, tail.cpu(), w.cpu(), 1e-6)
+    ref.assert_within(dw, dwr, ref.norm_dw_bound(mw, T), "dweight")

@@ -130,6 +130,41 @@ def test_experts_match_64_bits(T, H, E, I, k, shared, group, clip):
     ref.assert_within(out, want, bound, "out")
 
 
+# contractions so long that a chunk holds fewer rows than a column tile, down to
+# one, with the rows behind it read but not stored
+@pytest.mark.parametrize("T,H,I,group", [(21, 20480, 128, 64), (19, 128, 20480, 32),
+                                         (5, 65536, 128, 128), (40, 128, 65536, 128)])
+def test_long_contractions(T, H, I, group):
+    p = problem(T, H, 2, I, 1, 1, 0.0)
+    q, s = draw_packed(2, p, group, 30, std=0.01)
+    sq, ss = draw_packed(1, p, group, 31, std=0.01)
+    idx, w = draw_routing(T, 2, 1, 32)
+    x = torch.randn(T, H, generator=torch.Generator().manual_seed(33)).to(BF)
+    out = run_experts(p, group, x, idx, w, q, s, sq, ss)
+    sh = ref.w4_weights(sq, ss, I, H, group)[0]
+    want, bound = ref.w4_layer(x, idx, w, ref.w4_weights(q, s, I, H, group), sh, 0.0, group)
+    ref.assert_within(out, want, bound, "out")
+
+
+def test_codes_past_4_gigabytes():
+    # the last expert's codes start behind byte 2^32: the same expert alone gives
+    # the same rows (E = 16 of 302 MB each; the products' order does not depend on E)
+    H, I, E = 16384, 12288, 16
+    per = 3 * I * H
+    g = torch.Generator(device=DEV).manual_seed(40)
+    q = torch.randint(0, 256, (E, per // 2), generator=g, dtype=torch.uint8, device=DEV)
+    s = ((0.5 + torch.rand(E, per // 128, generator=g, device=DEV)) * 0.002).to(BF)
+    assert (E - 1) * (per // 2) > 1 << 32
+    x = torch.randn(3, H, generator=g, device=DEV).to(BF)
+    w = torch.rand(3, 1, generator=g, device=DEV)
+    outs = []
+    for n, e in ((E, E - 1), (1, 0)):
+        idx = torch.full((3, 1), e, dtype=torch.int32, device=DEV)
+        p = problem(3, H, n, I, 1)
+        outs.append(run_experts(p, 128, x, idx, w, q[E - n:], s[E - n:], None, None))
+    assert torch.equal(*outs) and torch.isfinite(outs[0]).all() and (outs[0] != 0).any()
+
+
 def test_clamp_saturates():
     p = problem(12, 256, 4, 128, 2, 1, 2.5)
     q, s = draw_packed(4, p, 128, 6, std=2.0)

@@ -41,7 +41,7 @@ def R(p):
     return ctypes.byref(p.c())
 
 
-def norm(lib, p=None, x=A, res=A, w=A, eps=1e-6, ro=A, y=A, q=A, s=A):
+def norm(lib, p=None, x=A, res=A, w=A, eps=1e-6, ro=2 * A, y=A, q=A, s=A):
     return lib.moe_add_rmsnorm(R(p or problem()), P(x), P(res), P(w), eps, P(ro), P(y), P(q), P(s),
                                None)
 
@@ -51,6 +51,7 @@ def test_norm_refusals(lib):
     assert norm(lib, x=0) == bad and norm(lib, w=0) == bad
     assert norm(lib, y=0, q=0, s=0) == bad                    # nothing to write
     assert norm(lib, q=0) == bad and norm(lib, s=0) == bad    # codes without scales
+    assert norm(lib, ro=A) == bad                             # both outputs in one buffer
     for name in ("x", "res", "w", "ro", "y", "q"):
         assert norm(lib, **{name: A + 8}) == bad, name
     for eps in (-1e-6, math.nan, math.inf):
@@ -106,7 +107,7 @@ def test_balance_loss_refusals(lib):
     assert call(n=need - 1) == moe.MOE_ERR_WORKSPACE
 
     def back(n_seq=5, **kw):
-        a = {k: P(v) for k, v in {**dict(logits=A, off=A, counts=A, tokens=A, grad=A, dl=A),
+        a = {k: P(v) for k, v in {**dict(logits=A, off=A, counts=A, tokens=A, grad=A, dl=2 * A),
                                   **kw}.items()}
         return lib.moe_balance_loss_backward(R(p), a["logits"], None, None, a["off"], n_seq,
                                              a["counts"], a["tokens"], a["grad"], a["dl"], None)
@@ -114,6 +115,7 @@ def test_balance_loss_refusals(lib):
     for name in ("logits", "off", "counts", "tokens", "grad", "dl"):
         assert back(**{name: 0}) == moe.MOE_ERR_INVALID_ARG, name
     assert back(n_seq=-1) == moe.MOE_ERR_INVALID_ARG
+    assert back(dl=A) == moe.MOE_ERR_INVALID_ARG           # the logits are still read
 
 
 def test_w4_refusals(lib):
