@@ -258,10 +258,10 @@ W4Layout w4_layout(const moe_problem* p, bool with_route) {
 
 // 8-row column tiles per task, from the mean rows per expert: one leaves registers
 // for 16 warps, two read a weight once for 16 rows.  Measured (256 experts of
-// 6144 x 2048, groups of 64), one against two tiles: 0.91 and 1.02 ms at 96 tokens
-// (3 rows), 1.15 and 1.18 at 192 (6), 1.47 and 1.40 at 256 (8), 2.75 and 2.60 at
-// 512.
-int w4_column_tiles(double mean_rows) { return mean_rows <= 7.0 ? 1 : 2; }
+// 6144 x 2048, groups of 64, calls in a row), one against two tiles: 0.93 and 1.04
+// ms at 96 tokens (3 rows), 1.04 and 1.09 at 128 (4), 1.18 and 1.14 at 160 (5),
+// 1.56 and 1.39 at 256, 2.75 and 2.50 at 512.
+int w4_column_tiles(double mean_rows) { return mean_rows <= 4.5 ? 1 : 2; }
 
 int w4_cap(int nt, int64_t K, int sub) {
     if (sub == 1) return nt == 1 ? w4_rows_cap<1, 1>(K) : w4_rows_cap<2, 1>(K);

@@ -208,54 +208,34 @@ struct W4Sched {
         rows[kMaxSegments];
 };
 
-// Shares of the run that chunks of one and of two column tiles are worth: with
-// equal shares the CTAs that met two large chunks set the time of a T = 256 batch.
-constexpr int kW4CostOne = 5, kW4CostTwo = 8;
-
-// cost[g] = sum of the chunk costs of the segments before g, by one warp.
-__device__ __forceinline__ void w4_cost_prefix(const W4Sched& sp, int nseg, int cap,
-                                               int32_t* cost) {
-    const int lane = threadIdx.x & 31;
-    int before = 0;
-    for (int s0 = 0; s0 < nseg; s0 += 32) {
-        const int s = s0 + lane;
-        int v = 0;
-        if (s < nseg && sp.rows[s] > 0) {
-            const int full = sp.prefix[s + 1] - sp.prefix[s] - 1;  // chunks before the last
-            v = full * (cap <= 8 ? kW4CostOne : kW4CostTwo) +
-                (sp.rows[s] - full * cap <= 8 ? kW4CostOne : kW4CostTwo);
-        }
-        int x = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (s < nseg) cost[s] = before + x - v;
-        before += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (lane == 0) cost[nseg] = before;
+// What a chunk of so many rows counts for when the CTAs share out the tasks.  With
+// equal shares the CTAs that met the larger chunks set the time: their loads come
+// later than the others', which take the memory's bandwidth meanwhile.
+constexpr int kW4CostFew = 3, kW4CostOne = 5, kW4CostTwo = 8;
+template <int NT>
+__device__ __forceinline__ int w4_cost(int rows) {
+    if (NT == 1) return rows <= 4 ? kW4CostFew : kW4CostOne;
+    return rows <= 8 ? kW4CostOne : kW4CostTwo;
 }
 
-// First task that starts at place x or behind it, of cost[nseg] * tiles places.
+// First task that starts at place x or behind it; a segment s with its tiles takes
+// the places from cost[s] * tiles on.
+template <int NT>
 __device__ __forceinline__ int64_t w4_task_at(const W4Sched& sp, const int32_t* cost, int nseg,
                                               int cap, int tiles, int64_t x) {
-    if (x >= static_cast<int64_t>(cost[nseg]) * tiles)
-        return static_cast<int64_t>(sp.prefix[nseg]) * tiles;
+    const int at = static_cast<int>(x / tiles);
+    if (at >= cost[nseg]) return static_cast<int64_t>(sp.prefix[nseg]) * tiles;
     int lo = 0, hi = nseg - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (static_cast<int64_t>(cost[mid]) * tiles <= x) lo = mid;
+        if (cost[mid] <= at) lo = mid;
         else hi = mid - 1;
     }
-    x -= static_cast<int64_t>(cost[lo]) * tiles;
-    const int chunks = sp.prefix[lo + 1] - sp.prefix[lo];
-    const int full = cap <= 8 ? kW4CostOne : kW4CostTwo;
-    const int j = static_cast<int>(min(x / (static_cast<int64_t>(full) * tiles),
-                                       static_cast<int64_t>(chunks - 1)));
-    x -= static_cast<int64_t>(j) * full * tiles;
-    const int own = sp.rows[lo] - j * cap <= 8 ? kW4CostOne : kW4CostTwo;
-    return static_cast<int64_t>(sp.prefix[lo] + j) * tiles + (x + own - 1) / own;
+    const int chunks = sp.prefix[lo + 1] - sp.prefix[lo], full = w4_cost<NT>(cap);
+    const int j = min((at - cost[lo]) / full, chunks - 1);
+    const int rest = static_cast<int>(x - static_cast<int64_t>(cost[lo] + j * full) * tiles);
+    const int own = w4_cost<NT>(min(cap, sp.rows[lo] - j * cap));
+    return static_cast<int64_t>(sp.prefix[lo] + j) * tiles + (rest + own - 1) / own;
 }
 
 // A round of a CTA: `tiles` tiles from `tile` on of one chunk of rows (chunk
@@ -342,18 +322,26 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
     __syncthreads();
     // this CTA's run of tasks
     int64_t begin, end;
-    if constexpr (NT == 1) {
-        const int64_t total = static_cast<int64_t>(sp.prefix[args.nseg]) * args.tiles;
-        begin = total * blockIdx.x / gridDim.x;
-        end = total * (blockIdx.x + 1) / gridDim.x;
-    } else {
+    {
         __shared__ int32_t cost[kMaxSegments + 1];
-        if (warp == 0) w4_cost_prefix(sp, args.nseg, cap, cost);
+        __shared__ int s_warp[32];
+        int v = 0;
+        if (threadIdx.x < args.nseg && sp.rows[threadIdx.x] > 0) {
+            // chunks before the segment's last
+            const int full = sp.prefix[threadIdx.x + 1] - sp.prefix[threadIdx.x] - 1;
+            v = full * w4_cost<NT>(cap) + w4_cost<NT>(sp.rows[threadIdx.x] - full * cap);
+        }
+        int all = 0;
+        const int before = block_exclusive_scan(v, s_warp, &all);
+        if (threadIdx.x < args.nseg) cost[threadIdx.x] = before;
+        if (threadIdx.x == args.nseg) cost[args.nseg] = all;
         __syncthreads();
-        const int64_t total = static_cast<int64_t>(cost[args.nseg]) * args.tiles;
-        begin = w4_task_at(sp, cost, args.nseg, cap, args.tiles, total * blockIdx.x / gridDim.x);
-        end = w4_task_at(sp, cost, args.nseg, cap, args.tiles,
-                         total * (blockIdx.x + 1) / gridDim.x);
+        // (odd lanes find the end)
+        const int64_t x =
+            static_cast<int64_t>(all) * args.tiles * (blockIdx.x + (lane & 1)) / gridDim.x;
+        const int64_t task = w4_task_at<NT>(sp, cost, args.nseg, cap, args.tiles, x);
+        begin = __shfl_sync(0xffffffffu, task, 0);
+        end = __shfl_sync(0xffffffffu, task, 1);
     }
     const int run = static_cast<int>(end - begin);
     if (run == 0) {
@@ -467,8 +455,11 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
         // offsets of the lane's row r and of its columns' sums and scales (rows
         // past the chunk's last hold anything: their columns are not stored)
         const int kb0 = (warp & ((1 << cur.log_ks) - 1)) * nkb >> cur.log_ks;
-        uint32_t b = (kb0 * cap + r) * kW4RowBytes + (c ^ ((r & 1) * 4)) * 16;
-        uint32_t m = (kb0 * cap + 2 * c) * kMeta;
+        const bool few = NT == 1 && cur.nrows <= 4;
+        uint32_t b = few ? (kb0 * cap + (r & 3)) * kW4RowBytes +
+                               ((((r >> 2) ^ (r & 1)) << 2) | c) * 16
+                         : (kb0 * cap + r) * kW4RowBytes + (c ^ ((r & 1) * 4)) * 16;
+        uint32_t m = (kb0 * cap + 2 * (few ? c & 1 : c)) * kMeta;
         // Limbs of the lane's columns.  With 12 warps those past the chunk's rows
         // are zeros and not read, which saves power more than time (1.41 -> 1.37 ms a
         // call for 256 tokens in a row under the power limit); with 16 the loads
@@ -603,6 +594,63 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
             b += cap * kW4RowBytes;
             m += cap * kMeta;
         };
+        // One weight block against up to four rows: column r of the one tile is limb
+        // r / 4 of row r % 4, which halves the MMAs, conversions and reads.  The two
+        // limbs' sums stay apart until the end of the round.
+        auto block4 = [&](const W4Stage<SUB>& s) {
+            constexpr int kSums = w4_sums(SUB);
+            constexpr int kSteps = SUB == 4 ? 1 : (SUB == 2 ? 2 : 4);  // MMAs of a group
+            const uint32_t* p[2] = {s_meta + m, s_meta + m + kMeta};
+            int32_t acc[2][4];
+            float part[2][4];
+            uint4 v;
+#pragma unroll
+            for (int k32 = 0; k32 < 4; ++k32) {
+                if (k32 % 2 == 0)
+                    v = *reinterpret_cast<const uint4*>(s_rows + b + k32 * 64);
+                const int g = k32 / kSteps;
+                int32_t from[4];
+                if (k32 % kSteps == 0) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        from[j] = static_cast<int32_t>(p[j][2 * g + (c >> 1)]);
+                        if (SUB == 1) from[j] += static_cast<int32_t>(p[j][2 + (c >> 1)]);
+                        from[2 + j] = 16 * from[j];
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t w0 = s.a[h][2 * k32], w1 = s.a[h][2 * k32 + 1];
+                    const uint32_t f[4] = {w0 & 0x0f0f0f0fu, w0 & 0xf0f0f0f0u, w1 & 0x0f0f0f0fu,
+                                           w1 & 0xf0f0f0f0u};
+                    if (k32 % kSteps == 0)
+                        mma_u8s8(acc[h], f, (k32 & 1) ? v.z : v.x, (k32 & 1) ? v.w : v.y, from);
+                    else
+                        mma_u8s8(acc[h], f, (k32 & 1) ? v.z : v.x, (k32 & 1) ? v.w : v.y, acc[h]);
+                }
+                if (k32 % kSteps == kSteps - 1) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t sw = h ? s.s[g].y : s.s[g].x;
+                        const float2 sv =
+                            __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&sw));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float x = static_cast<float>(acc[h][i]), w = i < 2 ? sv.x : sv.y;
+                            part[h][i] = g == 0 ? w * x : fmaf(w, x, part[h][i]);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = __uint_as_float(p[i & 1][2 * kSums]) * (c < 2 ? 256.0f : 1.0f);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) tot[h][0][i] = fmaf(a, part[h][i], tot[h][0][i]);
+            }
+            b += cap * kW4RowBytes;
+            m += cap * kMeta;
+        };
         auto blocks = [&](auto tiles) {
 #pragma unroll 1
             for (int kb = 0; kb < mine.n; kb += kStages) {
@@ -612,13 +660,22 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
                         const int ahead = kb + i + kStages + S::kAhead;
                         if (ahead < mine.n) prefetch(mine, ahead);
                         else if (more) prefetch(then, ahead - mine.n);
-                        block(tiles, st[i]);
+                        if constexpr (decltype(tiles)::value == 0) block4(st[i]);
+                        else block(tiles, st[i]);
                         load(st[i], mine, kb + i + kStages);
                     }
                 }
             }
         };
-        if (NT == 1 || cur.nrows <= 8) blocks(std::integral_constant<int, 1>{});
+        if (few) {
+            blocks(std::integral_constant<int, 0>{});
+            // lane 4r + c (c < 2) adds the low limbs of its columns, those of lane + 2
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tot[h][0][i] += __shfl_xor_sync(0xffffffffu, tot[h][0][i], 2);
+        } else if (NT == 1 || cur.nrows <= 8) blocks(std::integral_constant<int, 1>{});
         else blocks(std::integral_constant<int, NT>{});
         // (the value of lane 4r + c, index i: row r + 8 (i / 2) of half h, column
         // 8n + 2c + i % 2; row r + 8 carries 16 u)

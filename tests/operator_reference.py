@@ -198,7 +198,10 @@ def w4_ffn(x, mats, clip, group):
     most a/2 <= 2^-14.9 amax.  Its sums over a group are exact integers; the
     two limbs are joined, scaled (two products) and added to the fp32 total, in
     K/group additions and 8 more over the warps: each of these steps is off by at
-    most 2^-24 of the magnitudes added so far.  The clamp only shrinks errors;
+    most 2^-24 of the magnitudes added so far.  For chunks of up to four rows the
+    limbs' sums stay apart and are joined at the end of K: as a value v a = (256 hi
+    + lo) a has |lo| <= 128, the magnitudes are 256 |hi| a + |lo| a <= |v| a + 256 a,
+    and 256 a <= amax 256/16191 < amax/63.  The clamp only shrinks errors;
     |silu'| <= 1.1; exp, sum and quotient: 2^-20 of h."""
     gate, up, down = mats
     H, I = gate.shape[1], gate.shape[0]
@@ -209,7 +212,8 @@ def w4_ffn(x, mats, clip, group):
 
     def product(v, dv, m):
         e = (m.shape[1] / group + 8 + 3) * 2.0 ** -24
-        return v @ m.T, dv @ m.abs().T + e * ((v.abs() + dv) @ m.abs().T)
+        limbs = dv * (2.0 ** 14.9 / 63)
+        return v @ m.T, dv @ m.abs().T + e * ((v.abs() + dv + limbs) @ m.abs().T)
 
     x = x.to(F64)
     g, dg = product(x, floor(x), gate)
