@@ -283,7 +283,7 @@ int32_t launch_w4_n(const W4Args& a, int64_t max_tasks, cudaStream_t s) {
             return MOE_ERR_CUDA;
         configured.fetch_or(bit);
     }
-    const int smem = 2 * W4Shape<NT, SUB>::kSumBytes + W4Shape<NT, SUB>::kSlack +
+    const int smem = W4Shape<NT, SUB>::kSumBytes + W4Shape<NT, SUB>::kSlack +
                      a.K / kW4Block * a.cap * (kW4RowBytes + 4 * w4_meta_words(SUB));
     const int grid =
         static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sm_count(), max_tasks)));

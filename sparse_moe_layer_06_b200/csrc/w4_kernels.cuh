@@ -53,10 +53,9 @@ template <int NT, int SUB>
 struct W4Shape {
     static constexpr int kWarps = NT == 1 && SUB < 4 ? 16 : 12;
     static constexpr int kMostLog = kWarps == 16 ? 4 : 3;  // log2 of the warps that share a tile
-    static constexpr int kStages = 2;  // weight blocks a warp has on the way in registers
-    static constexpr int kAhead = 1;   // blocks that L2 has on the way for it
+    static constexpr int kAhead = NT;  // blocks behind its next one that L2 has on the way
     static constexpr int kVals = 2 * NT * 4 * 32;         // fp32 sums of a tile
-    static constexpr int kSumBytes = kWarps * kVals * 4;  // a buffer of them
+    static constexpr int kSumBytes = 2 * kWarps * kVals * 4;  // two buffers of them
     static constexpr int kSlack = 8 * NT * kW4RowBytes;   // rows read past the last block
 };
 
@@ -73,7 +72,7 @@ template <int NT, int SUB>
 int w4_rows_cap(int64_t K) {
     using S = W4Shape<NT, SUB>;
     const int64_t row = K / kW4Block * (kW4RowBytes + 4 * w4_meta_words(SUB));
-    const int64_t cap = (220 * 1024 - 2 * S::kSumBytes - S::kSlack) / row;
+    const int64_t cap = (220 * 1024 - S::kSumBytes - S::kSlack) / row;
     return static_cast<int>(cap < 8 * NT ? cap : 8 * NT);
 }
 
@@ -288,19 +287,21 @@ __device__ __forceinline__ void w4_next_round(W4Round& p, const W4Sched& sp, int
 // cost more than the weights, 700 against 456 us for the gate/up weights of 222
 // experts (2.9 GB).  2^log_ks warps share a tile, each with a part of its
 // blocks; their fp32 sums are added in shared memory in warp order.  The weights
-// stream through registers, kStages blocks ahead and across rounds, past L1; that
-// covers the way from L2, and a prefetch kAhead blocks further that from memory
-// (further ahead costs more than it hides: 445 us with 1, 449 with 2, 474 with 6,
-// 459 without).
+// stream through registers past L1, one block at a time and across rounds, with a
+// prefetch of the next kAhead blocks into L2.  (Two or three blocks in registers
+// were slower, 1.39 and 1.54 against 1.33 ms for 256 tokens: they cost spills, and
+// the warps cover the way from L2.  Further ahead costs more than it hides: 434 us
+// with 1, 440 with 2, 462 with 4 for the gate/up of 64 tokens; two column tiles,
+// 1.38 ms with 1, 1.33 with 2, 1.34 with 4 for 256 tokens.)
 template <int NT, bool DOWN, int SUB>
 __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
     w4_product_kernel(const W4Args args) {
     using S = W4Shape<NT, SUB>;
-    constexpr int kWarps = S::kWarps, kStages = S::kStages, kVals = S::kVals;
+    constexpr int kWarps = S::kWarps, kVals = S::kVals;
     constexpr int kMeta = w4_meta_words(SUB);
     extern __shared__ __align__(128) uint8_t s_dyn[];
     float(*s_sum)[kWarps][kVals] = reinterpret_cast<float(*)[kWarps][kVals]>(s_dyn);
-    uint8_t* s_rows = s_dyn + 2 * S::kSumBytes;  // [block][cap rows][256]
+    uint8_t* s_rows = s_dyn + S::kSumBytes;  // [block][cap rows][256]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, c = lane & 3;
     const int nkb = args.K / kW4Block, cap = args.cap;
@@ -388,8 +389,8 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
         w.n = slot < p.tiles ? ((part + 1) * nkb >> p.log_ks) - kb0 : 0;
         return w;
     };
-    W4Stage<SUB> st[kStages];
-    auto load = [&](W4Stage<SUB>& s, const Part& w, int i) {
+    W4Stage<SUB> s;
+    auto load = [&](const Part& w, int i) {
         if (i < w.n) {
             const uint8_t* p = w.q + static_cast<int64_t>(i) * kW4BlockBytes + lane * 32;
             ldg_stream(p, s.a[0]);
@@ -430,9 +431,8 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
                 s_meta[((i / kMeta) * cap + row) * kMeta + i % kMeta] = meta[i];
         }
     };
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) load(st[i], mine, i);
-    for (int i = kStages; i < kStages + S::kAhead; ++i) prefetch(mine, i);
+    load(mine, 0);
+    for (int i = 1; i <= S::kAhead; ++i) prefetch(mine, i);
     if constexpr (DOWN) ptx::grid_dep_wait();  // (the weights and the schedule are older)
     fetch_rows(cur);
     ptx::cp_async_wait_all();
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
             for (int l = 0; l < 2; ++l)
                 if (kLive) bv[n][l] = make_uint4(0, 0, 0, 0);
         // one weight block against N column tiles (those that the chunk has rows for)
-        auto block = [&](auto tiles, const W4Stage<SUB>& s) {
+        auto block = [&](auto tiles) {
             constexpr int N = decltype(tiles)::value;
             constexpr int kSums = w4_sums(SUB);
             // with one column tile the accumulators of both halves fit, a whole
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
         // One weight block against up to four rows: column r of the one tile is limb
         // r / 4 of row r % 4, which halves the MMAs, conversions and reads.  The two
         // limbs' sums stay apart until the end of the round.
-        auto block4 = [&](const W4Stage<SUB>& s) {
+        auto block4 = [&]() {
             constexpr int kSums = w4_sums(SUB);
             constexpr int kSteps = SUB == 4 ? 1 : (SUB == 2 ? 2 : 4);  // MMAs of a group
             const uint32_t* p[2] = {s_meta + m, s_meta + m + kMeta};
@@ -653,18 +653,13 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
         };
         auto blocks = [&](auto tiles) {
 #pragma unroll 1
-            for (int kb = 0; kb < mine.n; kb += kStages) {
-#pragma unroll
-                for (int i = 0; i < kStages; ++i) {
-                    if (kb + i < mine.n) {
-                        const int ahead = kb + i + kStages + S::kAhead;
-                        if (ahead < mine.n) prefetch(mine, ahead);
-                        else if (more) prefetch(then, ahead - mine.n);
-                        if constexpr (decltype(tiles)::value == 0) block4(st[i]);
-                        else block(tiles, st[i]);
-                        load(st[i], mine, kb + i + kStages);
-                    }
-                }
+            for (int kb = 0; kb < mine.n; ++kb) {
+                const int ahead = kb + 1 + S::kAhead;
+                if (ahead < mine.n) prefetch(mine, ahead);
+                else if (more) prefetch(then, ahead - mine.n);
+                if constexpr (decltype(tiles)::value == 0) block4();
+                else block(tiles);
+                load(mine, kb + 1);
             }
         };
         if (few) {
@@ -725,8 +720,7 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
         const bool other_rows = more && next.group != cur.group;
         if (more) {
             mine = then;
-#pragma unroll
-            for (int i = 0; i < kStages; ++i) load(st[i], mine, i);
+            load(mine, 0);
         }
         // (two buffers of sums in turn: the barrier of the next round that uses one
         // lies between this round's reads and the writes of the one after)
