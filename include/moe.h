@@ -452,8 +452,9 @@ int32_t moe_quantize_weights_w4(const moe_problem* problem, int32_t group_size,
  * moe_experts_w4 -- the layer behind its router, with 4-bit expert weights:
  *   out[t] = sum_j topk_w[t,j] * FFN_{topk_idx[t,j]}(x[t])  (+ shared FFN(x[t]))
  * dispatch, gate/up + clamp + SwiGLU, down, and the fixed-order combine in
- * fp32 (reproducible).  For decoding: the products are bound by reading the
- * weights of the touched experts up to about 8 rows per expert.
+ * fp32 (reproducible).  For decoding: the time is that of reading the touched
+ * experts' weights up to about 4 rows per expert, and grows with the rows from
+ * there on.
  *   x, out [T, H] bf16; topk_idx [T, top_k] int32 (a token's experts distinct);
  *   topk_w [T, top_k] fp32; expert_q, expert_scale: E experts;
  *   shared_q, shared_scale: 1 expert, or NULL when num_shared == 0.

@@ -27,8 +27,15 @@
 // with both words of a, the A fragments of one MMA.
 // Scales: [tile][block][r 8][128/G][half][r, r + 8] bf16.
 // Limbs of a row and block, 256 bytes: [a / 2][limb][c 4][a % 2][8 bytes], the 8
-// bytes in the order of the two words; in an array of their own the limb sums of
-// each group (two int16) and the scale, W4Meta words per row and block.
+// bytes in the order of the two words; in an array of their own the multiples of
+// the limb sums and the scale, w4_meta_words words per row and block.
+//
+// Measured, with 256 experts of 6144 x 2048, eight per token, and a shared one: 64
+// tokens take 427 and 229 us for the two products (2.9 and 1.45 GB of codes and
+// scales: 6.8 and 6.4 TB/s), 256 tokens 750 and 393 us, where the issue slots bound
+// (55% of the cycles with 3 warps a scheduler, each waiting mostly on its own
+// previous instruction; DRAM at 53%).  One token: 28 and 19 us for 9 experts, of
+// which 17 and 9 are the weights' share and the rest the start of each launch.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -47,8 +54,9 @@ constexpr int kW4MaxK = 65536;      // longest contraction (a row's limbs: 147 K
 
 // Shape of a launch whose tasks have up to 8 NT rows, in groups of 128 / SUB: one
 // CTA per SM.  One column tile leaves 128 registers a thread and so 16 warps; two,
-// or the scales of groups of 32, take up to 168 (110 and 63 us with 12 warps, 121
-// and 69 with 16, for 37 tokens of 32 experts of 7168 x 2048).
+// or the scales of groups of 32, take up to 168 (for 37 tokens of 32 experts of
+// 7168 x 2048 and groups of 32 the two products took a tenth longer with 16 warps;
+// for 256 tokens and two column tiles 14 warps take a fifth longer than 12).
 template <int NT, int SUB>
 struct W4Shape {
     static constexpr int kWarps = NT == 1 && SUB < 4 ? 16 : 12;
@@ -284,15 +292,15 @@ __device__ __forceinline__ void w4_next_round(W4Round& p, const W4Sched& sp, int
 // tile), each a pair tile against the chunk's rows.  The chunk's limbs lie in
 // shared memory (16-byte piece p of a row and block at p ^ 4 (row % 2), so that
 // the 8 lanes of a read meet different banks): taken through L1 instead, they
-// cost more than the weights, 700 against 456 us for the gate/up weights of 222
-// experts (2.9 GB).  2^log_ks warps share a tile, each with a part of its
-// blocks; their fp32 sums are added in shared memory in warp order.  The weights
-// stream through registers past L1, one block at a time and across rounds, with a
-// prefetch of the next kAhead blocks into L2.  (Two or three blocks in registers
-// were slower, 1.39 and 1.54 against 1.33 ms for 256 tokens: they cost spills, and
-// the warps cover the way from L2.  Further ahead costs more than it hides: 434 us
-// with 1, 440 with 2, 462 with 4 for the gate/up of 64 tokens; two column tiles,
-// 1.38 ms with 1, 1.33 with 2, 1.34 with 4 for 256 tokens.)
+// cost more than the weights (700 us for the gate/up of 64 tokens).  2^log_ks
+// warps share a tile, each with a part of its blocks; their fp32 sums are added in
+// shared memory in warp order.  The weights stream through registers past L1, one
+// block at a time and across rounds, with a prefetch of the next kAhead blocks into
+// L2.  (Two or three blocks in registers were slower, 1.39 and 1.54 against 1.33 ms
+// a call for 256 tokens: they cost spills, and the warps cover the way from L2.
+// Further ahead costs more than it hides: 434 us with 1, 440 with 2, 462 with 4 for
+// the gate/up of 64 tokens; with two column tiles 1.38 ms a call with 1, 1.33 with
+// 2, 1.34 with 4 for 256 tokens.)
 template <int NT, bool DOWN, int SUB>
 __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
     w4_product_kernel(const W4Args args) {
@@ -461,9 +469,9 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
                          : (kb0 * cap + r) * kW4RowBytes + (c ^ ((r & 1) * 4)) * 16;
         uint32_t m = (kb0 * cap + 2 * (few ? c & 1 : c)) * kMeta;
         // Limbs of the lane's columns.  With 12 warps those past the chunk's rows
-        // are zeros and not read, which saves power more than time (1.41 -> 1.37 ms a
-        // call for 256 tokens in a row under the power limit); with 16 the loads
-        // would come late (0.82 -> 0.85 ms for 64 tokens).
+        // are zeros and not read, which saves power more than time (3% of a call for
+        // 256 tokens, calls in a row under the power limit); with 16 the loads would
+        // come late (3% more for 64 tokens).
         constexpr bool kLive = kWarps == 12;
         uint4 bv[NT][2];
 #pragma unroll
