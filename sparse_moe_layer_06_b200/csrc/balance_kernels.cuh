@@ -116,6 +116,27 @@ __device__ __forceinline__ void numerators(const float* __restrict__ bias, int E
     for (int i = 0; i < NP; ++i) l[i] = exp2_approx((l[i] - mx) * kLog2e);
 }
 
+// Adds a token, its logits l and the lane's selection e, to the lane's sums of
+// probabilities and the CTA's counts.
+template <int NP, bool VEC>
+__device__ __forceinline__ void add_token(const float* __restrict__ bias, int E, int k, int e,
+                                          float (&l)[NP], float (&acc)[NP], int32_t* s_cnt,
+                                          int32_t* status) {
+    if ((threadIdx.x & 31) < k) {
+        if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
+        else set_device_error(status, DEV_ERR_BAD_INDEX);
+    }
+    numerators<NP, VEC>(bias, E, l);
+    float z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) z += l[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) acc[i] = fmaf(l[i], inv, acc[i]);
+}
+
 // Floats from one slot of partial sums to the next: whole 16-byte vectors.
 __host__ __device__ constexpr int balance_pad(int E) { return (E + 3) & ~3; }
 
@@ -172,19 +193,7 @@ __global__ void __launch_bounds__(256, 3) balance_partial_kernel(
             for (int u = 0; u < kBalBatch; ++u) {
                 if (!(live >> u & 1)) continue;
                 ++ntok;
-                if (lane < k) {
-                    if (e[u] >= 0 && e[u] < E) atomicAdd(&s_cnt[e[u]], 1);
-                    else set_device_error(status, DEV_ERR_BAD_INDEX);
-                }
-                numerators<NP, VEC>(bias, E, l[u]);
-                float z = 0.0f;
-#pragma unroll
-                for (int i = 0; i < NP; ++i) z += l[u][i];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-                const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-#pragma unroll
-                for (int i = 0; i < NP; ++i) acc[i] = fmaf(l[u][i], inv, acc[i]);
+                add_token<NP, VEC>(bias, E, k, e[u], l[u], acc, s_cnt, status);
             }
         }
         if (lane == 0 && ntok) atomicAdd(&s_tok, ntok);
@@ -329,6 +338,94 @@ __global__ void __launch_bounds__(kBalFinal) balance_final_kernel(
         }
         tokens[n_seq] = used;
         *loss = used > 0 ? static_cast<float>(a / used) : 0.0f;
+    }
+}
+
+// Both passes for one sequence of a small batch, in one CTA of 16 warps: warp w
+// takes every 16th token from w on, and the warps' sums are added in fp64 in warp
+// order.
+constexpr int kBalOneWarps = 16;
+
+template <int NP, bool VEC>
+__global__ void __launch_bounds__(kBalOneWarps * 32) balance_one_kernel(
+    const float* __restrict__ logits, const float* __restrict__ bias,
+    const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask,
+    const int32_t* __restrict__ offsets, int64_t T, int E, int k, float* __restrict__ P_out,
+    int32_t* __restrict__ counts, int32_t* __restrict__ tokens, float* __restrict__ loss,
+    int32_t* status) {
+    __shared__ float s_sum[kBalOneWarps][kMaxExperts];
+    __shared__ int32_t s_cnt[kMaxExperts];
+    __shared__ double s_red[kBalOneWarps];
+    __shared__ int32_t s_n[kBalOneWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid < kMaxExperts) s_cnt[tid] = 0;
+    __syncthreads();
+    ptx::grid_dep_wait();
+    int64_t o0 = 0, o1 = T;
+    if (offsets) {
+        o0 = offsets[0];
+        o1 = offsets[1];
+        if (o0 < 0 || o1 < o0 || o1 > T) {
+            if (tid == 0) set_device_error(status, DEV_ERR_BAD_INDEX);
+            o1 = o0 = 0;  // counts as empty
+        }
+    }
+    float acc[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) acc[i] = 0.0f;
+    int ntok = 0;
+    for (int64_t t = o0 + warp; t < o1; t += kBalOneWarps * kBalBatch) {
+        float l[kBalBatch][NP];
+        int e[kBalBatch];
+        bool live[kBalBatch];
+#pragma unroll
+        for (int u = 0; u < kBalBatch; ++u) {
+            const int64_t at = t + u * kBalOneWarps;
+            live[u] = at < o1 && (!mask || mask[at]);
+            if (live[u]) {
+                e[u] = lane < k ? idx[at * k + lane] : 0;
+                load_slots<NP, VEC>(logits + at * E, E, -INFINITY, l[u]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kBalBatch; ++u) {
+            if (!live[u]) continue;
+            ++ntok;
+            add_token<NP, VEC>(bias, E, k, e[u], l[u], acc, s_cnt, status);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int x = slot_expert<VEC>(i);
+        if (x < E) s_sum[warp][x] = acc[i];
+    }
+    if (lane == 0) s_n[warp] = ntok;
+    __syncthreads();
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < kBalOneWarps; ++w) n += s_n[w];
+    double prod = 0.0;
+    if (tid < E) {
+        double p = 0.0;
+#pragma unroll
+        for (int w = 0; w < kBalOneWarps; ++w) p += s_sum[w][tid];
+        p = n > 0 ? p / n : 0.0;
+        const int32_t c = s_cnt[tid];
+        P_out[tid] = static_cast<float>(p);
+        counts[tid] = c;
+        if (n > 0) prod = p * (static_cast<double>(c) / (static_cast<double>(n) * k));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) prod += __shfl_xor_sync(0xffffffffu, prod, o);
+    if (lane == 0) s_red[warp] = prod;
+    __syncthreads();
+    if (tid == 0) {
+        double a = 0.0;
+#pragma unroll
+        for (int w = 0; w < kMaxExperts / 32; ++w) a += s_red[w];
+        tokens[0] = n;
+        tokens[1] = n > 0 ? 1 : 0;
+        *loss = static_cast<float>(a * E);
     }
 }
 

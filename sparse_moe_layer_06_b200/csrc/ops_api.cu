@@ -172,6 +172,11 @@ int balance_window(int64_t T) {
     return static_cast<int>(8 * std::max<int64_t>(1, (T + 8 * 444 - 1) / (8 * 444)));
 }
 
+// Up to this many tokens one sequence takes one CTA and one launch: 4.2 us a call
+// for 64 x 256 logits in a captured graph, 5.5 in two launches; 6.2 and 5.5 for 128
+// (called one by one, where the host bounds, 8.5 and 11.5 us for both).
+constexpr int64_t kBalOneTokens = 96;
+
 struct BalanceLayout {
     size_t status, ticket, part_p, part_c, part_n, seq_loss, total;
 };
@@ -502,6 +507,17 @@ int32_t moe_balance_loss(const moe_problem* p, const float* logits, const float*
     int32_t* part_c = at<int32_t>(ws, L.part_c);
     int32_t* part_n = at<int32_t>(ws, L.part_n);
     uint32_t* ticket = at<uint32_t>(ws, L.ticket);
+    if (n_seq == 1 && p->T <= kBalOneTokens)
+        return with_slots(p->E, aligned16(logits) && aligned16(bias),
+                          [&](auto np, auto vec) -> int32_t {
+            MOE_LAUNCH("balance_one", s,
+                       if (launch_ex(balance_one_kernel<decltype(np)::value, decltype(vec)::value>,
+                                     1, kBalOneWarps * 32, 0, s, pdl_enabled(), logits, bias,
+                                     topk_idx, token_mask, seq_offsets, p->T, p->E, p->top_k,
+                                     mean_prob, counts, tokens, loss, status) != cudaSuccess)
+                           return MOE_ERR_CUDA);
+            return MOE_OK;
+        });
     MOE_TRY(with_slots(p->E, aligned16(logits) && aligned16(bias),
                        [&](auto np, auto vec) -> int32_t {
         MOE_LAUNCH("balance_partial", s,

@@ -221,3 +221,24 @@ def test_tokens_past_the_32_bit_offset():
     d, mag = ref.balance_backward(logits, bias, None, None, rc, rt, 0.37, k)
     ref.assert_within(dl[T - n:], d, mag * (2 * units + 24) * 2.0 ** -24, "dlogits")
     assert not dl[:T - n].any()
+
+
+@pytest.mark.parametrize("T", [1, 15, 64, 95, 96, 97])
+@pytest.mark.parametrize("E,k", [(32, 2), (50, 3), (100, 4), (250, 8), (256, 8)])
+def test_small_batches_of_one_sequence(T, E, k):
+    # one launch up to 96 tokens: whole, inside offsets, empty, offsets out of range
+    args = draw(T, E, k, 14, 0.6, 0.3)
+    check(*args, None)
+    check(*args, [T // 3, T - T // 4])
+    check(*args, [T, T])
+    before = moe.moe_launch_count()
+    loss, counts, tokens, P = run_loss(*args, [0, T + 1], status=moe.MOE_ERR_BAD_INDEX)
+    assert moe.moe_launch_count() - before == (1 if T <= 96 else 2)
+    assert float(loss[0]) == 0 and tokens.tolist() == [0, 0] and not counts.any()
+    assert not P.any()
+    bad = args[2].clone()
+    bad[0, 0] = E
+    full = args[3].clone().fill_(1)
+    _, counts, tokens, _ = run_loss(args[0], args[1], bad, full, None,
+                                    status=moe.MOE_ERR_BAD_INDEX)
+    assert int(counts.sum()) == T * k - 1 and tokens.tolist() == [T, 1]
