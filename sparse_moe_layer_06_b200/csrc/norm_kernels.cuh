@@ -19,10 +19,6 @@ namespace moe {
 
 constexpr int kNormMaxH = 16384;
 
-// Most threads of a CTA whose threads hold VPT vectors of a row.
-template <typename T, int VPT>
-constexpr int kNormThreads = VPT == 2 || sizeof(T) == 2 ? 512 : 1024;
-
 // The 16-byte vector of values f rounded to the row type.
 template <typename T>
 __device__ __forceinline__ uint4 pack_vec(const float (&f)[16 / sizeof(T)]) {
@@ -177,8 +173,8 @@ __global__ void __launch_bounds__(128) add_rmsnorm_short_kernel(
 // the ring needs no barrier, and an output may overlay the inputs of the same
 // row.  (One row per CTA without the ring left the loads' latency in the open:
 // 65 us against 41 for 4096 rows of 6144 bf16 with residual and codes.)
-template <typename T, int VPT, int D>
-__global__ void __launch_bounds__(kNormThreads<T, VPT>) add_rmsnorm_kernel(
+template <typename T, int VPT, int D, int MaxThreads>
+__global__ void __launch_bounds__(MaxThreads) add_rmsnorm_kernel(
     const T* x, const T* res, const T* __restrict__ weight, float eps, int64_t n_rows, int H,
     T* res_out, T* y, uint8_t* y_q, float* __restrict__ y_scale) {
     constexpr int kVE = 16 / static_cast<int>(sizeof(T));
@@ -239,9 +235,12 @@ __global__ void __launch_bounds__(kNormThreads<T, VPT>) add_rmsnorm_kernel(
 
 // Backward over rows blockIdx.x, blockIdx.x + gridDim.x, ..., with the same ring:
 // dx of each row, and the CTA's share of dw, kept in registers (a thread owns the
-// same columns of every row) and written once to partial[blockIdx.x].
-template <typename T, int VPT, int D>
-__global__ void __launch_bounds__(kNormThreads<T, VPT>) add_rmsnorm_backward_kernel(
+// same columns of every row) and written once to partial[blockIdx.x].  Rows of
+// more than 1024 vectors take up to 1024 threads, so 64 registers each: a thread
+// with 16 columns reads its part of the ring once more instead of keeping it (at
+// 2048 rows of 12288 bf16 the spilled form took 87 us).
+template <typename T, int VPT, int D, int MaxThreads>
+__global__ void __launch_bounds__(MaxThreads) add_rmsnorm_backward_kernel(
     const T* dy, const T* dres, const T* h, const T* __restrict__ weight, float eps,
     int64_t n_rows, int H, T* dx, float* __restrict__ partial) {
     constexpr int kVE = 16 / static_cast<int>(sizeof(T));
@@ -249,6 +248,7 @@ __global__ void __launch_bounds__(kNormThreads<T, VPT>) add_rmsnorm_backward_ker
     __shared__ float s_red[2][64];
     const int tx = threadIdx.x, nt = blockDim.x;
     const int nv = H / kVE;
+    constexpr bool kReread = VPT * kVE == 16 && MaxThreads == 1024;
     uint4* ring = reinterpret_cast<uint4*>(s_ring);  // [D][h, dy, dres][nv]
     const int per_stage = (dres ? 3 : 2) * nv;
     ptx::grid_dep_wait();
@@ -285,25 +285,35 @@ __global__ void __launch_bounds__(kNormThreads<T, VPT>) add_rmsnorm_backward_ker
     int stage = 0, flip = 0;
     for (int64_t row = blockIdx.x; row < n_rows; row += gridDim.x, flip ^= 1) {
         ring_wait<D - 1>();
-        uint4 hv[VPT], gv[VPT], rv[VPT];
+        const uint4* in = ring + stage * per_stage;
+        const int from = stage;
+        uint4 kept[kReread ? 1 : VPT][3];
+        if constexpr (!kReread) {
 #pragma unroll
-        for (int u = 0; u < VPT; ++u) {
-            const int v = tx + u * nt;
-            hv[u] = gv[u] = rv[u] = make_uint4(0, 0, 0, 0);
-            if (v < nv) {
-                hv[u] = ring[stage * per_stage + v];
-                gv[u] = ring[stage * per_stage + nv + v];
-                if (dres) rv[u] = ring[stage * per_stage + 2 * nv + v];
+            for (int u = 0; u < VPT; ++u) {
+                const int v = tx + u * nt;
+                kept[u][0] = kept[u][1] = kept[u][2] = make_uint4(0, 0, 0, 0);
+                if (v < nv) {
+                    kept[u][0] = in[v];
+                    kept[u][1] = in[nv + v];
+                    if (dres) kept[u][2] = in[2 * nv + v];
+                }
             }
+            fill(row + static_cast<int64_t>(D) * gridDim.x, from);
         }
-        fill(row + static_cast<int64_t>(D) * gridDim.x, stage);
+        // vector u of h (0), dy (1) or dres (2)
+        auto get = [&](int which, int u) {
+            if constexpr (!kReread) return kept[u][which];
+            const int v = tx + u * nt;
+            return v < nv ? in[which * nv + v] : make_uint4(0, 0, 0, 0);
+        };
         if (++stage == D) stage = 0;
         float sq = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
             float hf[kVE], gf[kVE], wf[kVE];
-            unpack_vec<T>(hv[u], hf);
-            unpack_vec<T>(gv[u], gf);
+            unpack_vec<T>(get(0, u), hf);
+            unpack_vec<T>(get(1, u), gf);
             unpack_vec<T>(wv[u], wf);
 #pragma unroll
             for (int e = 0; e < kVE; ++e) {
@@ -318,10 +328,10 @@ __global__ void __launch_bounds__(kNormThreads<T, VPT>) add_rmsnorm_backward_ker
         for (int u = 0; u < VPT; ++u) {
             const int v = tx + u * nt;
             float hf[kVE], gf[kVE], wf[kVE], rf[kVE];
-            unpack_vec<T>(hv[u], hf);
-            unpack_vec<T>(gv[u], gf);
+            unpack_vec<T>(get(0, u), hf);
+            unpack_vec<T>(get(1, u), gf);
             unpack_vec<T>(wv[u], wf);
-            unpack_vec<T>(rv[u], rf);
+            unpack_vec<T>(dres ? get(2, u) : make_uint4(0, 0, 0, 0), rf);
 #pragma unroll
             for (int e = 0; e < kVE; ++e) {
                 dw[u][e] = fmaf(gf[e], hf[e] * r, dw[u][e]);
@@ -329,6 +339,7 @@ __global__ void __launch_bounds__(kNormThreads<T, VPT>) add_rmsnorm_backward_ker
             }
             if (v < nv) reinterpret_cast<uint4*>(dx + row * H)[v] = pack_vec<T>(rf);
         }
+        if constexpr (kReread) fill(row + static_cast<int64_t>(D) * gridDim.x, from);
     }
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {

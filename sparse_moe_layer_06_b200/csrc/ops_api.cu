@@ -26,20 +26,24 @@ int32_t check_norm(const moe_problem* p, float eps) {
 }
 
 // How a launch over rows of H values covers them: VPT 16-byte vectors per
-// thread (2 up to 1024 vectors, 4 above), CTAs per SM (about `per_sm` threads),
+// thread (2 up to `two` vectors, 4 above), CTAs per SM (about `per_sm` threads),
 // and the depth of their rings.
 struct RowShape {
     int nv, vpt, threads, ctas, depth, smem;
 };
 
 constexpr int kNormThreadsPerSM = 768, kNormBackThreadsPerSM = 512;
+// Longest rows that take two vectors per thread (longer ones four).  Forward: 100
+// us with two and 96 with four for 8192 rows of 4352 fp32.  Backward, which keeps
+// its share of dw too: 89 and 213 us.
+constexpr int kNormTwo = 1024, kNormBackTwo = 2048;
 constexpr int kRingBytesPerSM = 200 * 1024;
 
-RowShape row_shape(const moe_problem* p, int inputs, int per_sm) {
+RowShape row_shape(const moe_problem* p, int inputs, int per_sm, int two) {
     RowShape r;
     const int row_bytes = p->H * (p->dtype == MOE_BF16 ? 2 : 4);
     r.nv = row_bytes / 16;
-    r.vpt = r.nv <= 1024 ? 2 : 4;
+    r.vpt = r.nv <= two ? 2 : 4;
     r.threads = std::max(32, ((r.nv + r.vpt - 1) / r.vpt + 31) / 32 * 32);
     r.ctas = std::max(1, std::min(8, per_sm / r.threads));
     const int rows = kRingBytesPerSM / r.ctas / (inputs * row_bytes);
@@ -62,11 +66,11 @@ bool allow_ring(K kern, std::atomic<uint64_t>& configured) {
     return true;
 }
 
-template <typename T, int VPT, int D>
+template <typename T, int VPT, int D, int MaxThreads>
 int32_t launch_norm(const moe_problem* p, const RowShape& r, const void* x, const void* res,
                     const void* weight, float eps, void* res_out, void* y, uint8_t* y_q,
                     float* y_scale, cudaStream_t s) {
-    auto kern = add_rmsnorm_kernel<T, VPT, D>;
+    auto kern = add_rmsnorm_kernel<T, VPT, D, MaxThreads>;
     static std::atomic<uint64_t> configured{0};
     if (!allow_ring(kern, configured)) return MOE_ERR_CUDA;
     const int64_t most = static_cast<int64_t>(sm_count()) * r.ctas;
@@ -96,20 +100,21 @@ template <typename T>
 int32_t run_norm(const moe_problem* p, const void* x, const void* res, const void* weight,
                  float eps, void* res_out, void* y, uint8_t* y_q, float* y_scale,
                  cudaStream_t s) {
-    const RowShape r = row_shape(p, res ? 2 : 1, kNormThreadsPerSM);
+    const RowShape r = row_shape(p, res ? 2 : 1, kNormThreadsPerSM, kNormTwo);
     if (r.nv <= 64)
         return launch_norm_short<T, 2>(p, x, res, weight, eps, res_out, y, y_q, y_scale, s);
     if (r.nv <= 128)
         return launch_norm_short<T, 4>(p, x, res, weight, eps, res_out, y, y_q, y_scale, s);
-#define MOE_NORM(V, D) \
-    return launch_norm<T, V, D>(p, r, x, res, weight, eps, res_out, y, y_q, y_scale, s)
+#define MOE_NORM(V, D, N) \
+    return launch_norm<T, V, D, N>(p, r, x, res, weight, eps, res_out, y, y_q, y_scale, s)
+    constexpr int kMost = sizeof(T) == 2 ? 512 : 1024;  // threads of the widest row
     if (r.vpt == 2) {
-        if (r.depth == 4) MOE_NORM(2, 4);
-        MOE_NORM(2, 2);
+        if (r.depth == 4) MOE_NORM(2, 4, 512);
+        MOE_NORM(2, 2, 512);
     }
-    if (r.depth == 4) MOE_NORM(4, 4);
-    if (r.depth == 2) MOE_NORM(4, 2);
-    MOE_NORM(4, 1);
+    if (r.depth == 4) MOE_NORM(4, 4, kMost);
+    if (r.depth == 2) MOE_NORM(4, 2, kMost);
+    MOE_NORM(4, 1, kMost);
 #undef MOE_NORM
 }
 
@@ -119,16 +124,16 @@ int32_t run_norm(const moe_problem* p, const void* x, const void* res, const voi
 constexpr int64_t kNormBackSMs = 148;
 int64_t norm_backward_ctas(const moe_problem* p) {
     if (p->T <= 0) return 1;
-    const int64_t most = kNormBackSMs * row_shape(p, 3, kNormBackThreadsPerSM).ctas;
+    const int64_t most = kNormBackSMs * row_shape(p, 3, kNormBackThreadsPerSM, kNormBackTwo).ctas;
     const int64_t per = (p->T + most - 1) / most;
     return (p->T + per - 1) / per;
 }
 
-template <typename T, int VPT, int D>
+template <typename T, int VPT, int D, int MaxThreads>
 int32_t launch_norm_backward(const moe_problem* p, const RowShape& r, const void* dy,
                              const void* dres, const void* h, const void* weight, float eps,
                              void* dx, float* dweight, float* partial, cudaStream_t s) {
-    auto kern = add_rmsnorm_backward_kernel<T, VPT, D>;
+    auto kern = add_rmsnorm_backward_kernel<T, VPT, D, MaxThreads>;
     static std::atomic<uint64_t> configured{0};
     if (!allow_ring(kern, configured)) return MOE_ERR_CUDA;
     const int ctas = static_cast<int>(norm_backward_ctas(p));
@@ -149,16 +154,24 @@ template <typename T>
 int32_t run_norm_backward(const moe_problem* p, const void* dy, const void* dres, const void* h,
                           const void* weight, float eps, void* dx, float* dweight,
                           float* partial, cudaStream_t s) {
-    const RowShape r = row_shape(p, dres ? 3 : 2, kNormBackThreadsPerSM);
-#define MOE_NORM(V, D) \
-    return launch_norm_backward<T, V, D>(p, r, dy, dres, h, weight, eps, dx, dweight, partial, s)
-    if (r.vpt == 2) {
-        if (r.depth == 4) MOE_NORM(2, 4);
-        MOE_NORM(2, 2);
+    const RowShape r = row_shape(p, dres ? 3 : 2, kNormBackThreadsPerSM, kNormBackTwo);
+#define MOE_NORM(V, D, N) \
+    return launch_norm_backward<T, V, D, N>(p, r, dy, dres, h, weight, eps, dx, dweight, partial, s)
+    if (r.threads <= 512) {
+        if (r.depth == 4) MOE_NORM(2, 4, 512);
+        MOE_NORM(2, 2, 512);
     }
-    if (r.depth == 4) MOE_NORM(4, 4);
-    if (r.depth == 2) MOE_NORM(4, 2);
-    MOE_NORM(4, 1);
+    if (r.vpt == 2) {
+        if (r.depth == 4) MOE_NORM(2, 4, 1024);
+        if (r.depth == 2) MOE_NORM(2, 2, 1024);
+        MOE_NORM(2, 1, 1024);
+    }
+    if constexpr (sizeof(T) == 4) {
+        if (r.depth == 4) MOE_NORM(4, 4, 1024);
+        if (r.depth == 2) MOE_NORM(4, 2, 1024);
+        MOE_NORM(4, 1, 1024);
+    }
+    return MOE_ERR_UNSUPPORTED;
 #undef MOE_NORM
 }
 
