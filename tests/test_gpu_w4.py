@@ -219,6 +219,20 @@ def test_infinite_and_nan_rows_stay_theirs():
     assert torch.isnan(out[3]).all()
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_infinite_and_nan_rows_in_chunks_of_up_to_four(group):
+    p = problem(4, 256, 3, 128, 2, 1)
+    q, s = draw_packed(3, p, group, 34)
+    sq, ss = draw_packed(1, p, group, 35)
+    idx, w = draw_routing(4, 3, 2, 36)
+    x = torch.randn(4, 256, generator=torch.Generator().manual_seed(37)).to(BF)
+    clean = run_experts(p, group, x, idx, w, q, s, sq, ss)
+    x[1, 5], x[2, 200] = float("nan"), float("-inf")
+    out = run_experts(p, group, x, idx, w, q, s, sq, ss)
+    assert torch.equal(out[[0, 3]], clean[[0, 3]])
+    assert torch.isnan(out[[1, 2]]).all()
+
+
 def test_reproducible_and_rows_behind_the_batch_left():
     p = problem(50, 384, 8, 256, 3, 1)
     q, s = draw_packed(8, p, 64, 19)
