@@ -55,20 +55,22 @@ __device__ __forceinline__ float warp_max(float v) {
     return m;
 }
 
-// First sequence that ends behind token t (n_seq if none), by one warp: 32 places
-// of the range are looked at in each round, so up to 1024 sequences take two
-// loads, one behind the other.  Offsets that are not in order give some sequence
+// First sequence that ends behind token t (n_seq if none), by one warp: 64 places
+// of the range are looked at in each round, so up to 64 sequences take one load,
+// up to 4096 two, one behind the other.  Offsets that are not in order give some sequence
 // number, never one out of range.
 __device__ __forceinline__ int first_sequence(const int32_t* __restrict__ offsets, int n_seq,
                                               int64_t t) {
     const int lane = threadIdx.x & 31;
     int lo = 0, len = n_seq;
     while (len > 0) {
-        const int step = (len + 31) / 32;
+        const int step = (len + 63) / 64;
         // sequence lo + (lane + 1) step - 1 and all before it end at t or earlier?
-        const int at = (lane + 1) * step - 1;
+        const int at = (lane + 1) * step - 1, at2 = at + 32 * step;
         const bool before = at < len && offsets[lo + at + 1] <= t;
-        const int n = __popc(__ballot_sync(0xffffffffu, before));
+        const bool before2 = at2 < len && offsets[lo + at2 + 1] <= t;
+        const int n = __popc(__ballot_sync(0xffffffffu, before)) +
+                      __popc(__ballot_sync(0xffffffffu, before2));
         lo += n * step;
         len = step == 1 ? 0 : min(step - 1, len - n * step);
     }
@@ -217,22 +219,23 @@ __global__ void __launch_bounds__(256, 3) balance_partial_kernel(
     }
 }
 
-// Pass 2: CTA s adds the windows of sequence s (fp64, window order within each
-// of kBalGroups interleaved groups of 64 threads, four experts to a thread, then
-// group order) and writes its P, counts and token count; the CTA that finishes
-// last adds the sequences' losses in sequence order.
-constexpr int kBalGroups = 8;
-constexpr int kBalFinal = kBalGroups * kMaxExperts / 4;  // threads
+// Pass 2: CTA (s, c) adds the windows of sequence s for the experts from 4 g c on
+// (fp64, window order within each of kBalFinal / g interleaved groups of g threads,
+// four experts to a thread, then group order) and writes their P and counts, with
+// c = 0 the token count too; the CTA that finishes last adds all losses in order.
+// Few long sequences take narrow groups, so many of them: 2048 tokens of 32 experts
+// leave 256 windows to add.
+constexpr int kBalFinal = 512;  // threads
 
 __global__ void __launch_bounds__(kBalFinal) balance_final_kernel(
     const float* __restrict__ part_p, const int32_t* __restrict__ part_c,
     const int32_t* __restrict__ part_n, const int32_t* __restrict__ offsets, int n_seq, int64_t T,
-    int E, int k, int win, float* __restrict__ P_out, int32_t* __restrict__ counts,
+    int E, int k, int win, int log_g, float* __restrict__ P_out, int32_t* __restrict__ counts,
     int32_t* __restrict__ tokens, double* seq_loss, uint32_t* ticket, float* __restrict__ loss,
     int32_t* status) {
     constexpr int kWarps = kBalFinal / 32;
-    __shared__ __align__(16) double s_p[kBalGroups][kMaxExperts];
-    __shared__ __align__(16) int32_t s_c[kBalGroups][kMaxExperts];
+    __shared__ __align__(16) double s_p[kBalFinal * 4];   // [group][expert of the CTA]
+    __shared__ __align__(16) int32_t s_c[kBalFinal * 4];
     __shared__ double s_red[kWarps];
     __shared__ int32_t s_n[kWarps];
     __shared__ bool s_last;
@@ -248,15 +251,16 @@ __global__ void __launch_bounds__(kBalFinal) balance_final_kernel(
             o1 = o0 = 0;  // counts as empty
         }
     }
+    const int per = 4 << log_g, e0 = blockIdx.y * per;  // the CTA's experts
     const int64_t b0 = o0 / win, b1 = o1 > o0 ? (o1 - 1) / win : b0 - 1;
     {
-        const int g = tid / (kMaxExperts / 4), e = tid % (kMaxExperts / 4) * 4;
+        const int groups = kBalFinal >> log_g, e = e0 + (tid & ((1 << log_g) - 1)) * 4;
         const int pad = balance_pad(E);
         double p[4] = {0.0, 0.0, 0.0, 0.0};
         int4 c = make_int4(0, 0, 0, 0);
         if (e < pad) {
 #pragma unroll 8
-            for (int64_t b = b0 + g; b <= b1; b += kBalGroups) {
+            for (int64_t b = b0 + (tid >> log_g); b <= b1; b += groups) {
                 const float4 v = *reinterpret_cast<const float4*>(part_p + (b + s) * pad + e);
                 const int4 d = *reinterpret_cast<const int4*>(part_c + (b + s) * pad + e);
                 p[0] += v.x, p[1] += v.y, p[2] += v.z, p[3] += v.w;
@@ -264,8 +268,8 @@ __global__ void __launch_bounds__(kBalFinal) balance_final_kernel(
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s_p[g][e + i] = p[i];
-        *reinterpret_cast<int4*>(&s_c[g][e]) = c;
+        for (int i = 0; i < 4; ++i) s_p[tid * 4 + i] = p[i];
+        *reinterpret_cast<int4*>(&s_c[tid * 4]) = c;
     }
     int32_t n = 0;
     for (int64_t b = b0 + tid; b <= b1; b += kBalFinal) n += part_n[b + s];
@@ -277,14 +281,14 @@ __global__ void __launch_bounds__(kBalFinal) balance_final_kernel(
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) n += s_n[w];
     double prod = 0.0;
-    const int e = tid;
-    if (e < E) {
+    const int e = e0 + tid;
+    if (tid < per && e < E) {
         double p = 0.0;
         int32_t c = 0;
-#pragma unroll
-        for (int i = 0; i < kBalGroups; ++i) {
-            p += s_p[i][e];
-            c += s_c[i][e];
+#pragma unroll 8
+        for (int i = tid; i < kBalFinal * 4; i += per) {
+            p += s_p[i];
+            c += s_c[i];
         }
         p = n > 0 ? p / n : 0.0;
         P_out[static_cast<int64_t>(s) * E + e] = static_cast<float>(p);
@@ -299,25 +303,19 @@ __global__ void __launch_bounds__(kBalFinal) balance_final_kernel(
         double a = 0.0;
 #pragma unroll
         for (int w = 0; w < kMaxExperts / 32; ++w) a += s_red[w];
-        tokens[s] = n;
-        if (n_seq == 1) {
-            tokens[1] = n > 0 ? 1 : 0;
-            *loss = static_cast<float>(a * E);
-        } else {
-            seq_loss[s] = a * E;
-            __threadfence();
-            s_last = atomicAdd(ticket, 1u) == gridDim.x - 1;
-        }
+        if (blockIdx.y == 0) tokens[s] = n;
+        seq_loss[static_cast<int64_t>(s) * gridDim.y + blockIdx.y] = a * E;
+        __threadfence();
+        s_last = atomicAdd(ticket, 1u) == gridDim.x * gridDim.y - 1;
     }
-    if (n_seq == 1) return;
     __syncthreads();
     if (!s_last) return;
     __threadfence();
     double a = 0.0;
     int used = 0;
-    for (int i = tid; i < n_seq; i += kBalFinal) {
+    for (int64_t i = tid; i < static_cast<int64_t>(n_seq) * gridDim.y; i += kBalFinal) {
         a += __ldcg(seq_loss + i);
-        used += __ldcg(tokens + i) > 0 ? 1 : 0;
+        if (i < n_seq) used += __ldcg(tokens + i) > 0 ? 1 : 0;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {

@@ -127,10 +127,10 @@ T* at(void* ws, size_t off) {
 // serialization): the kernel must then wait (griddepcontrol.wait) before it
 // reads anything the previous launch writes.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_ex(void (*kern)(KArgs...), int grid, int threads, int smem, cudaStream_t s,
+cudaError_t launch_ex(void (*kern)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t s,
                       bool pdl, Args&&... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;

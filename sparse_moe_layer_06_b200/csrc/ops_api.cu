@@ -190,6 +190,18 @@ int balance_window(int64_t T) {
 // (called one by one, where the host bounds, 8.5 and 11.5 us for both).
 constexpr int64_t kBalOneTokens = 96;
 
+// log2 of the threads of pass 2 that share a window's experts, four each: eight or
+// sixteen, and so up to four CTAs a sequence, while these are no more than the SMs.
+int balance_log_group(int64_t E, int64_t n_seq) {
+    int g = E <= 32 ? 3 : 4;
+    while ((4 << g) < E && (E + (4 << g) - 1) / (4 << g) * n_seq > 148) ++g;
+    return g;
+}
+int64_t balance_chunks(int64_t E, int64_t n_seq) {
+    const int per = 4 << balance_log_group(E, n_seq);
+    return (E + per - 1) / per;
+}
+
 struct BalanceLayout {
     size_t status, ticket, part_p, part_c, part_n, seq_loss, total;
 };
@@ -204,7 +216,7 @@ BalanceLayout balance_layout(const moe_problem* p, int64_t n_seq) {
     L.part_p = c.take(slots * balance_pad(p->E) * 4);
     L.part_c = c.take(slots * balance_pad(p->E) * 4);
     L.part_n = c.take(slots * 4);
-    L.seq_loss = c.take(n_seq * 8);
+    L.seq_loss = c.take(n_seq * balance_chunks(p->E, n_seq) * 8);
     L.total = c.off;
     return L;
 }
@@ -542,13 +554,17 @@ int32_t moe_balance_loss(const moe_problem* p, const float* logits, const float*
         return MOE_OK;
     }));
     MOE_LAUNCH("balance_final", s,
-               if (launch_ex(balance_final_kernel, n_seq, kBalFinal, 0, s,
+               if (launch_ex(balance_final_kernel,
+                             dim3(static_cast<unsigned>(n_seq),
+                                  static_cast<unsigned>(balance_chunks(p->E, n_seq))),
+                             kBalFinal, 0, s,
                              pdl_enabled(), static_cast<const float*>(part_p),
                              static_cast<const int32_t*>(part_c),
                              static_cast<const int32_t*>(part_n), seq_offsets,
-                             static_cast<int>(n_seq), p->T, p->E, p->top_k, win, mean_prob, counts,
-                             tokens, at<double>(ws, L.seq_loss), ticket, loss, status) !=
-                   cudaSuccess) return MOE_ERR_CUDA);
+                             static_cast<int>(n_seq), p->T, p->E, p->top_k, win,
+                             balance_log_group(p->E, n_seq), mean_prob, counts, tokens,
+                             at<double>(ws, L.seq_loss), ticket, loss, status) != cudaSuccess)
+                   return MOE_ERR_CUDA);
     return MOE_OK;
 }
 
