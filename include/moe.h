@@ -386,7 +386,8 @@ int32_t moe_add_rmsnorm_backward(const moe_problem* problem, const void* dy,
  * throughout.  Sums are taken in a fixed order (reproducible).  Offsets out of
  * order and experts out of range set MOE_ERR_BAD_INDEX in the error word (such
  * a sequence counts as empty, such a selection not at all; where offsets go
- * down, what the other sequences give is not defined).  1 <= n_seq <= 2^20.  Workspace: moe_balance_loss_workspace_size(problem, n_seq)
+ * down, what the other sequences give is not defined).  1 <= n_seq <= 2^20.
+ * Workspace: moe_balance_loss_workspace_size(problem, n_seq)
  * (MOE_CALL_BALANCE_LOSS sizes it for n_seq = 1).
  */
 size_t moe_balance_loss_workspace_size(const moe_problem* problem, int32_t n_seq);
