@@ -242,3 +242,13 @@ def test_small_batches_of_one_sequence(T, E, k):
     _, counts, tokens, _ = run_loss(args[0], args[1], bad, full, None,
                                     status=moe.MOE_ERR_BAD_INDEX)
     assert int(counts.sum()) == T * k - 1 and tokens.tolist() == [T, 1]
+
+
+# the experts of a sequence in four, two and one CTAs of pass 2, with the last one
+# part full, and windows that many sequences share
+@pytest.mark.parametrize("E", [33, 100, 130, 256])
+@pytest.mark.parametrize("n_seq", [2, 37, 60, 100, 149])
+def test_wide_routers_over_many_sequences(E, n_seq):
+    g = torch.Generator().manual_seed(15)
+    cuts = torch.randint(0, 601, (n_seq - 1,), generator=g).sort().values.tolist()
+    check(*draw(600, E, 4, 16, 0.6, 0.2), [0] + cuts + [600])
