@@ -285,10 +285,10 @@ def _loss_backward_plain(s):
 def _unpack_w4(q, sc, tiles, blocks, group):
     """Packed codes [n, tiles*blocks*2048] and scales -> fp32 [n, tiles, 2, 16, 128*blocks]."""
     n = q.shape[0]
-    # [n, tile, block, half, r, c, k32, k4, khi, k2]; the low nibble is row r, the high row r + 8
-    u = q.view(n, tiles, blocks, 2, 8, 4, 4, 2, 2, 2)
+    # [n, tile, block, half, k64, r, c, k32, k4, khi, k2]; the low nibble is row r, the high r + 8
+    u = q.view(n, tiles, blocks, 2, 2, 8, 4, 2, 2, 2, 2)
     v = torch.stack([u & 15, u >> 4], dim=-1)
-    v = v.permute(0, 1, 3, 10, 4, 2, 6, 5, 7, 9, 8).reshape(n, tiles, 2, 16, 128 * blocks)
+    v = v.permute(0, 1, 3, 11, 5, 2, 4, 7, 6, 8, 10, 9).reshape(n, tiles, 2, 16, 128 * blocks)
     w = v.float().sub_(8.0)
     sub = 128 // group
     t = sc.view(n, tiles, blocks, 8, sub, 2, 2).permute(0, 1, 5, 6, 3, 2, 4)
@@ -351,6 +351,8 @@ def _handle(s):
             ws = moe.alloc_workspace(p, moe.MOE_CALL_ADD_RMSNORM_BACKWARD)
         elif c["op"] == "loss":
             ws = moe.alloc_balance_workspace(p, c["n_seq"])
+        elif c["op"] == "loss_backward":
+            ws = moe.alloc_workspace(p, moe.MOE_CALL_BALANCE_LOSS_BACKWARD)
         elif c["op"] == "w4":
             ws = moe.alloc_workspace(p, moe.MOE_CALL_EXPERTS_W4)
         s["handle"] = (moe, p, ws)
@@ -385,9 +387,9 @@ def _loss_own(s):
 
 
 def _loss_backward_own(s):
-    moe, p, _ = _handle(s)
+    moe, p, ws = _handle(s)
     moe.moe_balance_loss_backward(p, s["logits"], s["bias"], s["mask"], s["offsets"], s["counts"],
-                                  s["tokens"], s["grad"], s["dlogits"])
+                                  s["tokens"], s["grad"], s["dlogits"], ws)
     return {"dlogits": s["dlogits"]}
 
 
@@ -503,8 +505,9 @@ def _exact_weights(q, sc, row0, rows, K, group, base_q, base_s, pair_rows):
     tile, r = i // pair_rows, i % pair_rows + row0
     half, r16, blk, k = r // 16, r % 16, kk // 128, kk % 128
     lane = (r16 % 8) * 4 + k % 32 // 8
-    byte = k // 32 * 8 + k % 8 // 4 * 4 + k % 2 * 2 + k % 4 // 2
-    at = ((tile * (K // 128) + blk) * 2 + half) * 1024 + lane * 32 + byte
+    word = k % 64 // 32 * 2 + k % 8 // 4
+    byte = k % 2 * 2 + k % 4 // 2
+    at = ((tile * (K // 128) + blk) * 2 + half) * 1024 + k // 64 * 512 + lane * 16 + word * 4 + byte
     v = (q[base_q + at] >> (4 * (r16 // 8)).to(torch.uint8)) & 15
     sub = 128 // group
     sat = (((tile * (K // 128) + blk) * 8 + r16 % 8) * sub + k // group) * 4 + half * 2 + r16 // 8
