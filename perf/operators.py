@@ -351,12 +351,19 @@ def _handle(s):
             ws = moe.alloc_workspace(p, moe.MOE_CALL_ADD_RMSNORM_BACKWARD)
         elif c["op"] == "loss":
             ws = moe.alloc_balance_workspace(p, c["n_seq"])
-        elif c["op"] == "loss_backward":
-            ws = moe.alloc_workspace(p, moe.MOE_CALL_BALANCE_LOSS_BACKWARD)
         elif c["op"] == "w4":
             ws = moe.alloc_workspace(p, moe.MOE_CALL_EXPERTS_W4)
+            # a program lays its weights out once, when it loads them
+            s["codes"] = _lay_out(s["q"]), None if s["sq"] is None else _lay_out(s["sq"])
         s["handle"] = (moe, p, ws)
     return s["handle"]
+
+
+def _lay_out(q):
+    """The codes in the library's order, a lane's 32 bytes of a block's half in one place:
+    [.., k64, lane, 16 bytes] -> [.., lane, k64, 16 bytes]."""
+    n = q.shape[0]
+    return q.view(torch.int64).view(n, -1, 2, 32, 2).transpose(2, 3).reshape(n, -1).view(torch.uint8)
 
 
 def _norm_own(s):
@@ -387,16 +394,17 @@ def _loss_own(s):
 
 
 def _loss_backward_own(s):
-    moe, p, ws = _handle(s)
+    moe, p, _ = _handle(s)
     moe.moe_balance_loss_backward(p, s["logits"], s["bias"], s["mask"], s["offsets"], s["counts"],
-                                  s["tokens"], s["grad"], s["dlogits"], ws)
+                                  s["tokens"], s["grad"], s["dlogits"])
     return {"dlogits": s["dlogits"]}
 
 
 def _w4_own(s):
     moe, p, ws = _handle(s)
-    moe.moe_experts_w4(p, s["case"]["group"], s["x"], s["idx"], s["w"], s["q"], s["sc"], s["sq"],
-                       s["ssc"], s["out"], ws)
+    q, sq = s["codes"]
+    moe.moe_experts_w4(p, s["case"]["group"], s["x"], s["idx"], s["w"], q, s["sc"], sq, s["ssc"],
+                       s["out"], ws)
     return {"out": s["out"]}
 
 
