@@ -421,12 +421,16 @@ int32_t moe_balance_loss_backward(const moe_problem* problem, const float* logit
  *
  * Numerics.  The products take each token row (and each row of h, which is
  * fp32) in blocks of 128 values with a power-of-two scale a and 16-bit
- * integers: bf16 values down to 2^-7 of the block's largest magnitude are exact,
- * any other value is off by at most a/2, 2^-14.9 of that magnitude.  The integer
- * sums of a group are exact; scaled, they are added in fp32.  A row with a value
- * that is not finite gives NaN.  Group scales are for weights of ordinary size:
- * one above 2^90 can overflow an fp32 sum that smaller activations would bring
- * back into range.
+ * integers: bf16 values down to 2^-6 of the block's largest magnitude are exact,
+ * any other value is off by at most a/2, 2^-14.9 of that magnitude.  Where that
+ * would take more than 2^-9 of the 2-norm of the values below 1024 a, and these
+ * are 96 or more of the 128 (a few channels far above the rest), the remainders
+ * enter as a second integer: every value is then off by at most 2^-29.8 of the
+ * largest.  (Blocks whose largest magnitude is below 2^-112 keep a step of
+ * 2^-126 instead.)  The integer sums of a group are exact; scaled, they are added
+ * in fp32.  A row with a value that is not finite gives NaN.  Group scales are
+ * finite and for weights of ordinary size: one above 2^90 can overflow an fp32
+ * sum that smaller activations would bring back into range.
  *
  * Packed layout, per expert: 3*I*H/2 bytes of codes and 3*I*H/group_size
  * scales, the gate/up part (I*H bytes, 2*I*H/group_size scales) before the

@@ -254,7 +254,9 @@ int32_t check_w4(const moe_problem* p, int32_t group) {
 
 struct W4Layout {
     size_t status, route, idx, w, hist, base, counts, offsets, sched_gu, sched_dn, pos, src,
-        row_w, x_rows, x_meta, h, h_rows, h_meta, y, total;
+        row_w, h, y, total;
+    // integers of the rows of x and of h: limbs and sums, and the second ones
+    size_t x_limbs[2], x_meta[2], h_limbs[2], h_meta[2];
 };
 
 W4Layout w4_layout(const moe_problem* p, bool with_route) {
@@ -276,11 +278,13 @@ W4Layout w4_layout(const moe_problem* p, bool with_route) {
     L.pos = c.take(T * k * 4);
     L.src = c.take(T * k * 4);
     L.row_w = c.take(T * k * 4);
-    L.x_rows = c.take(T * H * 2);
-    L.x_meta = c.take(T * (H / kW4Block) * kW4MaxMeta * 4);
+    for (int i = 0; i < 2; ++i) {
+        L.x_limbs[i] = c.take(T * H * 2);
+        L.x_meta[i] = c.take(T * (H / kW4Block) * kW4MaxMeta * 4);
+        L.h_limbs[i] = c.take(T * (k + S) * I * 2);
+        L.h_meta[i] = c.take(T * (k + S) * (I / kW4Block) * kW4MaxMeta * 4);
+    }
     L.h = c.take(T * (k + S) * I * 4);
-    L.h_rows = c.take(T * (k + S) * I * 2);
-    L.h_meta = c.take(T * (k + S) * (I / kW4Block) * kW4MaxMeta * 4);
     L.y = c.take(T * (k + S) * H * 4);
     L.total = c.off;
     return L;
@@ -352,15 +356,18 @@ int32_t run_experts_w4(const moe_problem* p, int32_t group, const void* x, const
     const int cap_gu = w4_cap(nt, H, sub), cap_dn = w4_cap(nt, I, sub);
     const bool pdl = pdl_enabled();
     const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
-    uint8_t* x_rows = at<uint8_t>(ws, L.x_rows);
-    uint32_t* x_meta = at<uint32_t>(ws, L.x_meta);
+    W4Rows x_rows[2], h_rows[2];
+    for (int i = 0; i < 2; ++i) {
+        x_rows[i] = {at<uint8_t>(ws, L.x_limbs[i]), at<uint32_t>(ws, L.x_meta[i])};
+        h_rows[i] = {at<uint8_t>(ws, L.h_limbs[i]), at<uint32_t>(ws, L.h_meta[i])};
+    }
     const int64_t x_units = T * (H / kW4Block);
     if (T <= kPermTokens) {
         MOE_LAUNCH("dispatch_w4", s,
                    if (launch_ex(w4_dispatch_kernel, 1 + static_cast<int>((x_units + 15) / 16),
                                  512, 0, s, pdl, idx, w, static_cast<int>(T), p->E, p->top_k,
                                  p->num_shared, sg, cap_gu, sd, cap_dn, pos, src, row_w, status,
-                                 xb, x_units, sub, x_rows, x_meta) != cudaSuccess)
+                                 xb, x_units, sub, x_rows[0], x_rows[1]) != cudaSuccess)
                        return MOE_ERR_CUDA);
     } else {
         // (an assignment with an expert out of range keeps position -1)
@@ -372,7 +379,8 @@ int32_t run_experts_w4(const moe_problem* p, int32_t group, const void* x, const
         MOE_LAUNCH("split_rows_w4", s,
                    if (launch_ex(w4_split_kernel<__nv_bfloat16>,
                                  static_cast<int>((x_units + 7) / 8), 256, 0, s, pdl, xb, x_units,
-                                 sub, x_rows, x_meta) != cudaSuccess) return MOE_ERR_CUDA);
+                                 sub, x_rows[0], x_rows[1]) != cudaSuccess)
+                       return MOE_ERR_CUDA);
     }
     const int nseg = static_cast<int>(E + S);
     // at most this many chunks of `cap` rows over all segments
@@ -393,8 +401,8 @@ int32_t run_experts_w4(const moe_problem* p, int32_t group, const void* x, const
     a.q_shared = sq;
     a.sc_shared = static_cast<const __nv_bfloat16*>(ss);
     a.sched = sg;
-    a.rows = x_rows;
-    a.meta = x_meta;
+    a.rows = x_rows[0];
+    a.rest = x_rows[1];
     a.cap = cap_gu;
     a.K = static_cast<int32_t>(H);
     a.tiles = static_cast<int32_t>(I / 16);
@@ -402,19 +410,17 @@ int32_t run_experts_w4(const moe_problem* p, int32_t group, const void* x, const
     a.ld = static_cast<int32_t>(I);
     MOE_TRY(launch_w4<false>(nt, group, a, max_chunks(cap_gu) * a.tiles, s));
     const int64_t h_units = T * (k + S) * (I / kW4Block);
-    uint8_t* h_rows = at<uint8_t>(ws, L.h_rows);
-    uint32_t* h_meta = at<uint32_t>(ws, L.h_meta);
     MOE_LAUNCH("split_h_w4", s,
                if (launch_ex(w4_split_kernel<float>, static_cast<int>((h_units + 7) / 8), 256, 0,
-                             s, pdl, static_cast<const float*>(a.out), h_units, sub, h_rows, h_meta) !=
-                   cudaSuccess) return MOE_ERR_CUDA);
+                             s, pdl, static_cast<const float*>(a.out), h_units, sub, h_rows[0],
+                             h_rows[1]) != cudaSuccess) return MOE_ERR_CUDA);
     a.q = eq + I * H;
     a.sc = static_cast<const __nv_bfloat16*>(es) + 2 * I * H / group;
     a.q_shared = sq ? sq + I * H : nullptr;
     a.sc_shared = ss ? static_cast<const __nv_bfloat16*>(ss) + 2 * I * H / group : nullptr;
     a.sched = sd;
-    a.rows = h_rows;
-    a.meta = h_meta;
+    a.rows = h_rows[0];
+    a.rest = h_rows[1];
     a.cap = cap_dn;
     a.K = static_cast<int32_t>(I);
     a.tiles = static_cast<int32_t>(H / 32);

@@ -9,9 +9,20 @@
 // bf16 fragment takes 7, and ran the first form of these kernels into the ALU
 // pipe, which has half rate).  A token row is split, per block of 128 values,
 // into a power-of-two scale a and 16-bit integers v = 256 hi + lo with two s8
-// limbs: bf16 values down to 2^-7 of the block's largest are exact, smaller ones
-// off by at most a / 2, 2^-15 of the largest, far inside the bf16 output's
-// rounding.  With the sums of the limbs of each group,
+// limbs: bf16 values down to 2^-6 of the block's largest are exact, smaller ones
+// off by at most a / 2, 2^-14.9 of the largest.  On rows without outliers that is
+// far inside the bf16 output's rounding (4e-6 of an output against 1.7e-3).  Beside
+// an outlier it is not: 1000 times the others, which hidden states have, and an
+// output whose weight there is 0 was off by 1%.  So where the values below 1024 a are
+// three quarters of a block or more and lose more than 2^-9 of their norm (about what
+// bf16 takes of fp32 values), the block is marked: the remainders x - a v, exact in
+// fp32, are split in the same way into a second integer with a scale of its own, and
+// a chunk's blocks with such a row are taken a second time; a value is then off by at
+// most 2^-29.8 of the block's largest.  (Of 10^6 blocks of normally, uniformly or
+// exponentially distributed values, or of products of such, none is marked.  64
+// tokens, 256 experts: 673 us a call for ordinary rows, 797 with three such channels
+// in every row, 1056 with eight; the code for it costs ordinary rows 0 to 3%.)
+// With the sums of the limbs of each group,
 //   sum_k (u_k - 8) s x_k = s a (256 (sum u hi - 8 sum hi) + (sum u lo - 8 sum lo)):
 // the accumulators start from -8 times the limb sums, and the joined integer,
 // below 2^29, is converted, scaled and added to the fp32 total once per group.
@@ -28,7 +39,8 @@
 // Scales: [tile][block][r 8][128/G][half][r, r + 8] bf16.
 // Limbs of a row and block, 256 bytes: [a / 2][limb][c 4][a % 2][8 bytes], the 8
 // bytes in the order of the two words; in an array of their own the multiples of
-// the limb sums and the scale, w4_meta_words words per row and block.
+// the limb sums, the scale and whether there is a second integer (whose limbs and
+// sums lie in two more such arrays), w4_meta_words words per row and block.
 //
 // Measured, with 256 experts of 6144 x 2048, eight per token, and a shared one: 64
 // tokens take 427 and 229 us for the two products (2.9 and 1.45 GB of codes and
@@ -68,11 +80,19 @@ struct W4Shape {
 };
 
 // Beside a row's block stand -8 times the sums of its two limbs over each group
-// of at most 64 values (w4_sums of them: a pair of int32 each), then the scale;
-// words of that per row and block, whole 16-byte vectors.
+// of at most 64 values (w4_sums of them: a pair of int32 each), then the scale and
+// the mark of a second integer (0 or 1); words of that per row and block, whole
+// 16-byte vectors.
 __host__ __device__ constexpr int w4_sums(int sub) { return sub == 4 ? 4 : 2; }
 __host__ __device__ constexpr int w4_meta_words(int sub) { return sub == 4 ? 12 : 8; }
+__host__ __device__ constexpr int w4_mark(int sub) { return 2 * w4_sums(sub) + 1; }
 constexpr int kW4MaxMeta = 12;
+
+// The integers of rows: limbs, and group sums with scales.
+struct W4Rows {
+    uint8_t* limbs;
+    uint32_t* meta;
+};
 
 // Rows of K values that fit beside the sums and the schedule (5 KB) in a CTA's
 // shared memory, at most 8 NT.
@@ -92,8 +112,7 @@ struct W4Args {
     int64_t q_stride, sc_stride;  // bytes / scales from one expert to the next
     const int32_t* sched;      // tile schedule of nseg segments (chunk j: rows from j * cap)
     int32_t nseg, special;
-    const uint8_t* rows;       // limbs of the token rows
-    const uint32_t* meta;      // their group sums and scales
+    W4Rows rows, rest;         // the token rows' integers, and the second ones
     const int32_t* row_src;    // gate/up: token of each routed row (special: the row itself)
     int32_t K, tiles, cap;     // contraction length, pair tiles, rows of a chunk
     float* out;                // gate/up: h rows, down: weighted rows; fp32 [*, ld]
@@ -135,27 +154,18 @@ struct W4Stage {
     uint2 s[SUB];      // [group]: half 0's and half 1's scales of rows r and r + 8
 };
 
-// Row block `unit` of rows in [*, K] order, by one warp: lane l has the values
-// 4 l .. 4 l + 3.  The scale is the power of two a with 16191 <= amax / a <=
-// 32384, which leaves both limbs of rint(x / a) in range (32640 would need 128).
-// A block with a value that is not finite gets a NaN scale, so its row's results
-// are NaN.
-template <typename T>
-__device__ __forceinline__ void w4_split_block(const T* __restrict__ rows, int sub, int64_t unit,
-                                               uint8_t* __restrict__ out,
-                                               uint32_t* __restrict__ meta) {
+// The four values v of each lane (128 of a block) as the integers rint(v / a) of one
+// scale, by one warp, and what is left of them in v.  The scale is the power of two a
+// with 16191 <= amax / a <= 32384, which leaves both limbs in range (32640 would need
+// 128).  A block with a value that is not finite gets a NaN scale, so its row's results
+// are NaN.  Returns whether the block is marked: at most 32 values from 1024 a on, and
+// the others lose more than 2^-9 of their 2-norm.  (An output's weights are hardly 0 at
+// more than 32 larger values; a block of 128 normally distributed ones has 111 to 119 of
+// them, and without that condition 2.5e-5 of such blocks would be marked, a few in each
+// call for 256 tokens, each of which held its CTA up by 100 us.)
+__device__ __forceinline__ bool w4_split_values(float (&v)[4], int sub, uint8_t* __restrict__ out,
+                                                uint32_t* __restrict__ meta) {
     const int lane = threadIdx.x & 31;
-    float v[4];
-    const T* in = rows + unit * kW4Block + lane * 4;
-    if constexpr (sizeof(T) == 2) {
-        const uint2 q = *reinterpret_cast<const uint2*>(in);
-        const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q.x));
-        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q.y));
-        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
-    } else {
-        const float4 q = *reinterpret_cast<const float4*>(in);
-        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-    }
     float amax = 0.0f;
     bool bad = false;
 #pragma unroll
@@ -173,19 +183,26 @@ __device__ __forceinline__ void w4_split_block(const T* __restrict__ rows, int s
     n = min(max(n, -126), 126);
     const float scale = __uint_as_float(static_cast<uint32_t>(n + 127) << 23);
     const float inv = __uint_as_float(static_cast<uint32_t>(127 - n) << 23);
-    meta += unit * w4_meta_words(sub);
-    out += unit * kW4RowBytes + (lane >> 4) * 128 + ((lane & 7) >> 1) * 16 + ((lane >> 3) & 1) * 8 + (lane & 1) * 4;
+    out += (lane >> 4) * 128 + ((lane & 7) >> 1) * 16 + ((lane >> 3) & 1) * 8 + (lane & 1) * 4;
     uint32_t hi = 0, lo = 0;
     int sum_hi = 0, sum_lo = 0;
+    float off = 0.0f;  // sum of (u - t)^2 - 2^-18 u^2 over the small u = v / a
+    int large = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int t = bad ? 0 : __float2int_rn(v[i] * inv);
+        const float u = v[i] * inv;
+        const int t = bad ? 0 : __float2int_rn(u);
         const int l = static_cast<int8_t>(t & 0xff), h = (t - l) >> 8;
         const int at = ((i & 1) << 1) | (i >> 1);  // bytes k, k + 2, k + 1, k + 3
         hi |= static_cast<uint32_t>(h & 0xff) << (8 * at);
         lo |= static_cast<uint32_t>(l & 0xff) << (8 * at);
         sum_hi += h;
         sum_lo += l;
+        const float rest = u - static_cast<float>(t);  // exact: |t| < 2^15, |rest| <= 1/2
+        const bool small = fabsf(u) < 1024.0f;
+        if (small) off += rest * rest - 0x1p-18f * (u * u);
+        large += __popc(__ballot_sync(0xffffffffu, !small));
+        v[i] = rest * scale;
     }
     *reinterpret_cast<uint32_t*>(out) = hi;
     *reinterpret_cast<uint32_t*>(out + 64) = lo;
@@ -197,16 +214,46 @@ __device__ __forceinline__ void w4_split_block(const T* __restrict__ rows, int s
     if (lane % per == 0)
         *reinterpret_cast<int2*>(meta + lane / per * 2) = make_int2(-8 * sum_hi, -8 * sum_lo);
     if (lane == 0) meta[2 * sums] = bad ? 0x7fc00000u : __float_as_uint(scale);
+    // (at the smallest scale the remainders would have no smaller one)
+    if (bad || n <= -126 || large > 32) return false;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) off += __shfl_xor_sync(0xffffffffu, off, o);
+    return off > 0.0f;
+}
+
+// Row block `unit` of rows in [*, K] order, by one warp: lane l has the values
+// 4 l .. 4 l + 3.
+template <typename T>
+__device__ __forceinline__ void w4_split_block(const T* __restrict__ rows, int sub, int64_t unit,
+                                               const W4Rows& out, const W4Rows& rest) {
+    const int lane = threadIdx.x & 31;
+    float v[4];
+    const T* in = rows + unit * kW4Block + lane * 4;
+    if constexpr (sizeof(T) == 2) {
+        const uint2 q = *reinterpret_cast<const uint2*>(in);
+        const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q.x));
+        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q.y));
+        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+    } else {
+        const float4 q = *reinterpret_cast<const float4*>(in);
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    }
+    const int64_t m = unit * w4_meta_words(sub);
+    const bool more = w4_split_values(v, sub, out.limbs + unit * kW4RowBytes, out.meta + m);
+    if (lane == 0) out.meta[m + w4_mark(sub)] = more ? 1 : 0;
+    if (more) {
+        w4_split_values(v, sub, rest.limbs + unit * kW4RowBytes, rest.meta + m);
+        if (lane == 0) rest.meta[m + w4_mark(sub)] = 1;
+    }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(256) w4_split_kernel(const T* __restrict__ rows, int64_t units,
-                                                       int sub, uint8_t* __restrict__ out,
-                                                       uint32_t* __restrict__ meta) {
+                                                       int sub, W4Rows out, W4Rows rest) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (unit < units) w4_split_block<T>(rows, sub, unit, out, meta);
+    if (unit < units) w4_split_block<T>(rows, sub, unit, out, rest);
 }
 
 // The tile schedule in shared memory.
@@ -315,6 +362,7 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
     const int nkb = args.K / kW4Block, cap = args.cap;
     uint32_t* s_meta = reinterpret_cast<uint32_t*>(s_rows + nkb * cap * kW4RowBytes);
     __shared__ W4Sched sp;
+    __shared__ uint32_t s_marks[kW4MaxK / kW4Block / 32];
     if constexpr (!DOWN) ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     {
@@ -423,30 +471,74 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
         }
     };
     Part mine = part_of(cur), then{};
-    // the chunk's rows into shared memory (asynchronous copies of this thread)
+    // the chunk's rows into shared memory (asynchronous copies of this thread); whether
+    // the thread met the mark of a second integer
     auto fetch_rows = [&](const W4Round& p) {
         const int first = sp.b_row0[p.seg] + p.row0;
         const bool direct = DOWN || p.seg == args.special;
+        bool marked = false;
         for (int row = warp; row < p.nrows; row += kWarps) {
             const int64_t m = (direct ? first + row : args.row_src[first + row]);
-            const uint8_t* src = args.rows + m * nkb * kW4RowBytes;
+            const uint8_t* src = args.rows.limbs + m * nkb * kW4RowBytes;
             for (int i = lane; i < nkb * 16; i += 32)
                 ptx::cp_async_16(s_rows + ((i >> 4) * cap + row) * kW4RowBytes +
                                      ((i & 15) ^ ((row & 1) * 4)) * 16,
                                  src + i * 16, 16);
-            const uint32_t* meta = args.meta + m * nkb * kMeta;
-            for (int i = lane; i < nkb * kMeta; i += 32)
-                s_meta[((i / kMeta) * cap + row) * kMeta + i % kMeta] = meta[i];
+            const uint32_t* meta = args.rows.meta + m * nkb * kMeta;
+            for (int i = lane; i < nkb * kMeta; i += 32) {
+                const uint32_t v = meta[i];
+                s_meta[((i / kMeta) * cap + row) * kMeta + i % kMeta] = v;
+                marked |= i % kMeta == w4_mark(SUB) && v != 0;
+            }
         }
+        return marked;
+    };
+    // bits of the blocks in which a row of the chunk in shared memory has a mark, by one warp
+    auto find_marks = [&](int nrows) {
+        for (int kb = 0; kb < nkb; kb += 32) {
+            uint32_t any = 0;
+            if (kb + lane < nkb)
+                for (int row = 0; row < nrows; ++row)
+                    any |= s_meta[((kb + lane) * cap + row) * kMeta + w4_mark(SUB)];
+            any = __ballot_sync(0xffffffffu, any != 0);
+            if (lane == 0) s_marks[kb / 32] = any;
+        }
+    };
+    // the marked blocks of the chunk's rows (asynchronous copies, a warp to a block and
+    // row): the second integers, 0 for rows without a mark, in the first ones' place, or
+    // the first ones again
+    auto fetch_marked = [&](const W4Round& p, const W4Rows& from, bool all) {
+        const int first = sp.b_row0[p.seg] + p.row0;
+        const bool direct = DOWN || p.seg == args.special;
+        int turn = 0;
+#pragma unroll 1
+        for (int word = 0; word * 32 < nkb; ++word)
+#pragma unroll 1
+            for (uint32_t w = s_marks[word]; w; w &= w - 1)
+#pragma unroll 1
+                for (int row = 0; row < p.nrows; ++row) {
+                    if (turn++ % kWarps != warp) continue;
+                    const int kb = word * 32 + __ffs(w) - 1, at = kb * cap + row;
+                    const int64_t m = direct ? first + row : args.row_src[first + row];
+                    const uint32_t has = all || s_meta[at * kMeta + w4_mark(SUB)] ? 16 : 0;
+                    if (lane < 16)
+                        ptx::cp_async_16(s_rows + at * kW4RowBytes + (lane ^ ((row & 1) * 4)) * 16,
+                                         from.limbs + (m * nkb + kb) * kW4RowBytes + lane * 16, has);
+                    else if (lane - 16 < kMeta / 4)
+                        ptx::cp_async_16(s_meta + at * kMeta + (lane - 16) * 4,
+                                         from.meta + (m * nkb + kb) * kMeta + (lane - 16) * 4, has);
+                }
     };
     load(mine, 0);
     for (int i = 1; i <= S::kAhead; ++i) prefetch(mine, i);
     if constexpr (DOWN) ptx::grid_dep_wait();  // (the weights and the schedule are older)
-    fetch_rows(cur);
+    bool marked = fetch_rows(cur);
     ptx::cp_async_wait_all();
-    __syncthreads();
+    marked = __syncthreads_or(marked);
 
-    for (int buffer = 0;;) {
+    // (a round over a chunk with marks goes round once more for each run of the warp's
+    // marked blocks; `start`, `at`: the first block at hand and the one behind, -1 before)
+    for (int buffer = 0, start = -1, at = -1;;) {
         const bool more = cur.left > 0;
         if (more) {
             next = cur;
@@ -464,10 +556,13 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
         // past the chunk's last hold anything: their columns are not stored)
         const int kb0 = (warp & ((1 << cur.log_ks) - 1)) * nkb >> cur.log_ks;
         const bool few = NT == 1 && cur.nrows <= 4;
-        uint32_t b = few ? (kb0 * cap + (r & 3)) * kW4RowBytes +
-                               ((((r >> 2) ^ (r & 1)) << 2) | c) * 16
-                         : (kb0 * cap + r) * kW4RowBytes + (c ^ ((r & 1) * 4)) * 16;
-        uint32_t m = (kb0 * cap + 2 * (few ? c & 1 : c)) * kMeta;
+        uint32_t b, m;
+        auto start_at = [&](int kb) {
+            b = few ? (kb * cap + (r & 3)) * kW4RowBytes + ((((r >> 2) ^ (r & 1)) << 2) | c) * 16
+                    : (kb * cap + r) * kW4RowBytes + (c ^ ((r & 1) * 4)) * 16;
+            m = (kb * cap + 2 * (few ? c & 1 : c)) * kMeta;
+        };
+        start_at(start < 0 ? kb0 : start);
         // Limbs of the lane's columns.  With 12 warps those past the chunk's rows
         // are zeros and not read, which saves power more than time (3% of a call for
         // 256 tokens, calls in a row under the power limit); with 16 the loads would
@@ -670,16 +765,17 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
                 load(mine, kb + 1);
             }
         };
+        if (few) blocks(std::integral_constant<int, 0>{});
+        else if (NT == 1 || cur.nrows <= 8) blocks(std::integral_constant<int, 1>{});
+        else blocks(std::integral_constant<int, NT>{});
         if (few) {
-            blocks(std::integral_constant<int, 0>{});
             // lane 4r + c (c < 2) adds the low limbs of its columns, those of lane + 2
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     tot[h][0][i] += __shfl_xor_sync(0xffffffffu, tot[h][0][i], 2);
-        } else if (NT == 1 || cur.nrows <= 8) blocks(std::integral_constant<int, 1>{});
-        else blocks(std::integral_constant<int, NT>{});
+        }
         // (the value of lane 4r + c, index i: row r + 8 (i / 2) of half h, column
         // 8n + 2c + i % 2; row r + 8 carries 16 u)
         auto store = [&](float g, float u, int tile, int h, int n, int i) {
@@ -703,7 +799,7 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
         };
         // a tile of one warp's own needs neither the sums nor the barrier
         const int ks = 1 << cur.log_ks, slot = warp >> cur.log_ks, part = warp & (ks - 1);
-        if (ks == 1) {
+        if (ks == 1 && !marked) {
             if (slot < cur.tiles) {
 #pragma unroll
                 for (int h = 0; h < (DOWN ? 2 : 1); ++h)
@@ -720,12 +816,48 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sums[((h * NT + n) * 4 + i) * 32 + lane] = tot[h][n][i];
+                    for (int i = 0; i < 4; ++i) {
+                        float& to = sums[((h * NT + n) * 4 + i) * 32 + lane];
+                        to = at < 0 ? tot[h][n][i] : to + tot[h][n][i];
+                    }
+        }
+        if (marked) {
+            const Part whole = part_of(cur);
+            if (at < 0) {
+                if (warp == 0) find_marks(cur.nrows);
+                __syncthreads();  // (and every warp is done with the rows)
+                fetch_marked(cur, args.rest, false);
+                at = kb0;
+                for (int kb = lane; kb < whole.n; kb += 32)
+                    if (s_marks[(kb0 + kb) >> 5] >> ((kb0 + kb) & 31) & 1)
+                        prefetch_l2(whole.q + static_cast<int64_t>(kb) * kW4BlockBytes,
+                                    kW4BlockBytes);
+                ptx::cp_async_wait_all();
+                __syncthreads();
+            }
+            uint32_t w = 0;
+            for (; at < kb0 + whole.n; at = (at | 31) + 1) {
+                w = s_marks[at >> 5] >> (at & 31);
+                if (w) break;
+            }
+            if (w) at += __ffs(w) - 1;
+            const int left = kb0 + whole.n - at;
+            if (left > 0) {
+                w >>= __ffs(w) - 1;
+                start = at;
+                mine.n = min(left, w == 0xffffffffu ? 32 : __ffs(~w) - 1);
+                mine.q = whole.q + static_cast<int64_t>(at - kb0) * kW4BlockBytes;
+                mine.sc = whole.sc + static_cast<int64_t>(at - kb0) * 64 * SUB;
+                at += mine.n;
+                load(mine, 0);
+                continue;
+            }
+            start = at = -1;
         }
         // the next round's first weights are on their way before this one is
         // added up, and its rows while it is
-        const bool other_rows = more && next.group != cur.group;
+        // (the second integers of a chunk took its marked blocks' place)
+        const bool other_rows = more && (next.group != cur.group || marked);
         if (more) {
             mine = then;
             load(mine, 0);
@@ -733,10 +865,14 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
         // (two buffers of sums in turn: the barrier of the next round that uses one
         // lies between this round's reads and the writes of the one after)
         if (ks > 1 || other_rows) __syncthreads();
-        if (other_rows) fetch_rows(next);
-        if (ks > 1) {
+        bool next_marked = marked;
+        if (other_rows) {
+            if (next.group != cur.group) next_marked = fetch_rows(next);
+            else fetch_marked(cur, args.rows, true);
+        }
+        if (ks > 1 || marked) {
             const float(*from)[kVals] = &s_sum[buffer][slot << cur.log_ks];
-            buffer ^= 1;
+            if (ks > 1) buffer ^= 1;
             constexpr int kOut = DOWN ? kVals : kVals / 2;
             for (int v = slot < cur.tiles ? part * 32 + lane : kOut; v < kOut; v += ks * 32) {
                 float g = 0.0f, u = 0.0f;
@@ -750,7 +886,7 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
         if (!more) break;
         if (other_rows) {
             ptx::cp_async_wait_all();
-            __syncthreads();
+            marked = __syncthreads_or(next_marked);
         }
         cur = next;
     }
@@ -766,13 +902,13 @@ __global__ void __launch_bounds__(512) w4_dispatch_kernel(
     int num_shared, int32_t* sched_gu, int nmax_gu, int32_t* sched_dn, int nmax_dn,
     int32_t* __restrict__ pos,
     int32_t* __restrict__ src, float* __restrict__ row_w, int32_t* status,
-    const __nv_bfloat16* __restrict__ x, int64_t units, int sub,
-    uint8_t* __restrict__ limbs, uint32_t* __restrict__ meta) {
+    const __nv_bfloat16* __restrict__ x, int64_t units, int sub, W4Rows x_rows,
+    W4Rows x_rest) {
     if (blockIdx.x > 0) {
         ptx::grid_dep_wait();
         ptx::grid_dep_launch();
         const int64_t unit = (static_cast<int64_t>(blockIdx.x) - 1) * 16 + (threadIdx.x >> 5);
-        if (unit < units) w4_split_block<__nv_bfloat16>(x, sub, unit, limbs, meta);
+        if (unit < units) w4_split_block<__nv_bfloat16>(x, sub, unit, x_rows, x_rest);
         return;
     }
     __shared__ uint32_t masks[kPermWarps][kMaxExperts];
