@@ -107,14 +107,15 @@ int32_t run_norm(const moe_problem* p, const void* x, const void* res, const voi
         return launch_norm_short<T, 4>(p, x, res, weight, eps, res_out, y, y_q, y_scale, s);
 #define MOE_NORM(V, D, N) \
     return launch_norm<T, V, D, N>(p, r, x, res, weight, eps, res_out, y, y_q, y_scale, s)
+    // (the other shapes belong to no width up to kNormMaxH)
     constexpr int kMost = sizeof(T) == 2 ? 512 : 1024;  // threads of the widest row
-    if (r.vpt == 2) {
-        if (r.depth == 4) MOE_NORM(2, 4, 512);
-        MOE_NORM(2, 2, 512);
+    if (r.vpt == 2 && r.depth == 4) MOE_NORM(2, 4, 512);
+    if (r.vpt == 4 && r.depth == 4) MOE_NORM(4, 4, kMost);
+    if (r.vpt == 4 && r.depth == 2) MOE_NORM(4, 2, kMost);
+    if constexpr (sizeof(T) == 4) {
+        if (r.vpt == 4) MOE_NORM(4, 1, 1024);
     }
-    if (r.depth == 4) MOE_NORM(4, 4, kMost);
-    if (r.depth == 2) MOE_NORM(4, 2, kMost);
-    MOE_NORM(4, 1, kMost);
+    return MOE_ERR_UNSUPPORTED;
 #undef MOE_NORM
 }
 
@@ -157,19 +158,13 @@ int32_t run_norm_backward(const moe_problem* p, const void* dy, const void* dres
     const RowShape r = row_shape(p, dres ? 3 : 2, kNormBackThreadsPerSM, kNormBackTwo);
 #define MOE_NORM(V, D, N) \
     return launch_norm_backward<T, V, D, N>(p, r, dy, dres, h, weight, eps, dx, dweight, partial, s)
-    if (r.threads <= 512) {
-        if (r.depth == 4) MOE_NORM(2, 4, 512);
-        MOE_NORM(2, 2, 512);
-    }
-    if (r.vpt == 2) {
-        if (r.depth == 4) MOE_NORM(2, 4, 1024);
-        if (r.depth == 2) MOE_NORM(2, 2, 1024);
-        MOE_NORM(2, 1, 1024);
-    }
+    // (the other shapes belong to no width up to kNormMaxH)
+    if (r.vpt == 2 && r.depth == 4 && r.threads <= 512) MOE_NORM(2, 4, 512);
+    if (r.vpt == 2 && r.depth == 4) MOE_NORM(2, 4, 1024);
+    if (r.vpt == 2 && r.depth == 2 && r.threads > 512) MOE_NORM(2, 2, 1024);
     if constexpr (sizeof(T) == 4) {
-        if (r.depth == 4) MOE_NORM(4, 4, 1024);
-        if (r.depth == 2) MOE_NORM(4, 2, 1024);
-        MOE_NORM(4, 1, 1024);
+        if (r.vpt == 4 && r.depth == 2) MOE_NORM(4, 2, 1024);
+        if (r.vpt == 4 && r.depth == 1) MOE_NORM(4, 1, 1024);
     }
     return MOE_ERR_UNSUPPORTED;
 #undef MOE_NORM
