@@ -435,9 +435,9 @@ __global__ void __launch_bounds__(kBalOneWarps * 32) balance_one_kernel(
 
 // Gradient of the loss.  Each warp takes `run` consecutive tokens, kBalBatch at
 // a time, and keeps the selection shares f of its current sequence in registers.
-// With c = 1/E, sum_j p_j (f_j - c) + c = sum_j p_j f_j: taking the shares
-// relative to the uniform one loses nothing of a small difference f - p.f to
-// rounding.
+// With c = 1/E, sum_j p_j (f_j - c) + c = sum_j p_j f_j: the shares are taken
+// relative to the uniform one, so that of a small difference f - p.f only the
+// rounding of f itself is lost, 2^-24 of f, and none of the sums'.
 template <int NP, bool VEC>
 __global__ void __launch_bounds__(256, 2) balance_backward_kernel(
     const float* __restrict__ logits, const float* __restrict__ bias,

@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(MaxThreads) add_rmsnorm_kernel(
 // same columns of every row) and written once to partial[blockIdx.x].  Rows of
 // more than 1024 vectors take up to 1024 threads, so 64 registers each: a thread
 // with 16 columns reads its part of the ring once more instead of keeping it (45 us
-// for 2048 rows of 12288 bf16; spilled, it took 87).  4096 rows of 6144 bf16 take
+// for 2048 rows of 12288 bf16; spilled, it took 87; the fp32 forms still spill 16 and
+// 36 bytes).  4096 rows of 6144 bf16 take
 // 37 us, 5.4 TB/s, and the sum over the CTAs 2 us more.
 template <typename T, int VPT, int D, int MaxThreads>
 __global__ void __launch_bounds__(MaxThreads) add_rmsnorm_backward_kernel(

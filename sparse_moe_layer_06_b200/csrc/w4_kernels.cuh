@@ -43,10 +43,10 @@
 // sums lie in two more such arrays), w4_meta_words words per row and block.
 //
 // Measured, with 256 experts of 6144 x 2048, eight per token, and a shared one: 64
-// tokens take 427 and 229 us for the two products (2.9 and 1.45 GB of codes and
-// scales: 6.8 and 6.4 TB/s), 256 tokens 750 and 393 us, where the issue slots bound
-// (55% of the cycles with 3 warps a scheduler, each waiting mostly on its own
-// previous instruction; DRAM at 53%).  One token: 28 and 19 us for 9 experts, of
+// tokens take 435 and 233 us for the two products (2.9 and 1.45 GB of codes and
+// scales: 6.7 and 6.2 TB/s), 256 tokens 784 and 402 us, where the issue slots bound
+// (53% of the cycles with 3 warps a scheduler, each waiting mostly on its own
+// previous instruction; DRAM at 51%).  One token: 28 and 19 us for 9 experts, of
 // which 17 and 9 are the weights' share and the rest the start of each launch.
 #pragma once
 
@@ -68,7 +68,9 @@ constexpr int kW4MaxK = 65536;      // longest contraction (a row's limbs: 147 K
 // CTA per SM.  One column tile leaves 128 registers a thread and so 16 warps; two,
 // or the scales of groups of 32, take up to 168 (for 37 tokens of 32 experts of
 // 7168 x 2048 and groups of 32 the two products took a tenth longer with 16 warps;
-// for 256 tokens and two column tiles 14 warps take a fifth longer than 12).
+// for 256 tokens and two column tiles 14 warps take a fifth longer than 12).  The
+// forms with two column tiles spill 20 to 106 bytes, that with one and groups of 64
+// spills 16.
 template <int NT, int SUB>
 struct W4Shape {
     static constexpr int kWarps = NT == 1 && SUB < 4 ? 16 : 12;
@@ -537,8 +539,8 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
     marked = __syncthreads_or(marked);
 
     // (a round over a chunk with marks goes round once more for each run of the warp's
-    // marked blocks; `start`, `at`: the first block at hand and the one behind, -1 before)
-    for (int buffer = 0, start = -1, at = -1;;) {
+    // marked blocks; `at`: the block behind the run at hand, -1 before the first)
+    for (int buffer = 0, at = -1;;) {
         const bool more = cur.left > 0;
         if (more) {
             next = cur;
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
                     : (kb * cap + r) * kW4RowBytes + (c ^ ((r & 1) * 4)) * 16;
             m = (kb * cap + 2 * (few ? c & 1 : c)) * kMeta;
         };
-        start_at(start < 0 ? kb0 : start);
+        start_at(at < 0 ? kb0 : at - mine.n);
         // Limbs of the lane's columns.  With 12 warps those past the chunk's rows
         // are zeros and not read, which saves power more than time (3% of a call for
         // 256 tokens, calls in a row under the power limit); with 16 the loads would
@@ -844,7 +846,6 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
             const int left = kb0 + whole.n - at;
             if (left > 0) {
                 w >>= __ffs(w) - 1;
-                start = at;
                 mine.n = min(left, w == 0xffffffffu ? 32 : __ffs(~w) - 1);
                 mine.q = whole.q + static_cast<int64_t>(at - kb0) * kW4BlockBytes;
                 mine.sc = whole.sc + static_cast<int64_t>(at - kb0) * 64 * SUB;
@@ -852,7 +853,7 @@ __global__ void __launch_bounds__(W4Shape<NT, SUB>::kWarps * 32, 1)
                 load(mine, 0);
                 continue;
             }
-            start = at = -1;
+            at = -1;
         }
         // the next round's first weights are on their way before this one is
         // added up, and its rows while it is
@@ -969,7 +970,10 @@ __global__ void __launch_bounds__(512) w4_dispatch_kernel(
     }
 }
 
-// Encoder: one CTA of 128 threads per 16-row half of a pair tile and block.
+// Encoder, for weights as they are loaded: one CTA of 128 threads per 16-row half of
+// a pair tile and block.  16 experts of 6144 x 2048 take 1.41 to 1.46 ms from bf16
+// and 1.47 to 1.54 from fp32, 1.1 and 1.8 TB/s (the down part reads 32 or 64 bytes
+// of a row at a time).
 // Row i of the half and k of the block come from in[...] with the strides of
 // the matrix (gate/up: k contiguous; down: rows contiguous).
 // scale = bf16(max |w| / 7) (1 where that is 0, NaN where the group holds a
