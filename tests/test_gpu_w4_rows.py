@@ -239,3 +239,43 @@ def test_what_is_exact(group, top):
     out = run_experts(p, group, x.to(BF), idx, w, q, s, None, None)
     want, bound = layer(x.to(BF), idx, w, ref.w4_weights(q, s, 128, 128, group), None, 0.0, group)
     ref.assert_within(out, want, bound, "out")
+
+
+@pytest.mark.parametrize("T", [4, 40, 300])
+def test_replays_on_rows_with_and_without_outliers(T):
+    # the marks are the rows' as they are at the replay, in one workspace, and two calls at
+    # once do not meet
+    p = problem(T, 384, 6, 256, 2, 1, 10.0)
+    q, s = draw_packed(6, p, 64, 75)
+    sq, ss = draw_packed(1, p, 64, 76)
+    idx, w = draw_routing(T, 6, 2, 77)
+    plain = torch.randn(T, 384, generator=torch.Generator().manual_seed(78))
+    hard = plain.clone()
+    hard[::2, 7], hard[::3, 300] = 2000.0, -700.0
+    batches = [plain.to(BF), hard.to(BF), plain.to(BF), hard.to(BF)]
+    want = [run_experts(p, 64, x, idx, w, q, s, sq, ss) for x in batches]
+    d = [t.to("cuda") for t in (idx, w, q, s, sq, ss)]
+    x, out = torch.empty_like(batches[0], device="cuda"), torch.empty_like(want[0])
+    ws = moe.alloc_workspace(p, moe.MOE_CALL_EXPERTS_W4)
+    x.copy_(batches[0])
+    call = lambda: moe.moe_experts_w4(p, 64, x, *d, out, ws)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for b, y in zip(batches, want):
+        x.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, y)
+    del graph
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    sets = [(b.to("cuda"), torch.empty_like(out), moe.alloc_workspace(p, moe.MOE_CALL_EXPERTS_W4))
+            for b in batches[:2]]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, (xs, o, wsp) in zip(streams, sets):
+            moe.moe_experts_w4(p, 64, xs, *d, o, wsp, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, y) for (_, o, _), y in zip(sets, want))
